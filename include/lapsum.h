@@ -430,6 +430,134 @@ int lapsum_shard_vjp_apply(const float* r, const float* v, int64_t n_shard, cons
 int lapsum_backward_noalloc(const float* r, int64_t ld, const double* b, const float* v, float* g,
                             int64_t B, int64_t n, double t, void* stream);
 
+/*
+ * Operators around a hard selection: routing tokens to experts, moving rows to
+ * the experts and back, attention over a cache that accumulates each key's
+ * weight, and eviction from that cache.  The pages name mixture-of-experts
+ * routing and memory selection as uses of a top-k operator (section 4.2) and
+ * give no algorithm for them; the definitions below are this library's.  These
+ * calls keep no state: no status word and no workspace_init, and a workspace, where
+ * one is needed, may hold anything before the call.
+ */
+
+/* Scores of lapsum_route. */
+enum lapsum_score {
+    LAPSUM_SCORE_SOFTMAX = 0, /* s = softmax of the row's logits */
+    LAPSUM_SCORE_SIGMOID = 1  /* s = 1 / (1 + e^-l), each logit by itself */
+};
+
+/*
+ * Expert routing, forward.  For each of T rows of E logits (`dtype`, row stride
+ * ld): scores s, keys c = s + bias (bias: E floats, or NULL for c = s), and the
+ * k experts with the largest keys, largest first, equal keys by the lower index.
+ * The order is that of the exact scores where there is no bias (equal logits
+ * tie), else of keys formed in fp64.  With top_groups < groups the E experts are
+ * `groups` runs of equal length, a group's value is the sum of its group_top (1 or
+ * 2) largest keys (of its only one, where it has one), and only experts of the
+ * top_groups groups with the largest values (ties: lower index) take part.
+ *     weights[t*k + j] = scale * s_j            (renormalize = 0)
+ *                      = scale * s_j / sum of the row's chosen s   (renormalize = 1)
+ * in fp32, experts[t*k + j] the expert, int32.  The bias moves the choice only.
+ * Renormalised weights keep their ratios where every chosen s underflows.
+ * An expert whose logit (or key) is -inf is never chosen; a row with fewer than
+ * k others gets expert -1 and weight 0 in the places left.  A row with a NaN or
+ * +inf logit, or a key that is one, gets experts -1 and weights NaN.
+ * 1 <= E <= 1024, 1 <= k <= min(32, top_groups * E / groups), groups <= 32 and a
+ * divisor of E, scale finite and > 0; else LAPSUM_EINVAL.
+ *
+ * lapsum_route_backward: dlogits (`dtype`, row stride ld_out) from dweights (T*k
+ * floats) and the forward's logits, weights and experts: the exact gradient with
+ * the choice held fixed.  Rows of NaN weights get NaN; dweights at expert -1 are
+ * not read.
+ */
+int lapsum_route(const void* logits, int dtype, int64_t ld, int64_t T, int64_t E, int32_t k,
+                 int score, const float* bias, int32_t groups, int32_t top_groups,
+                 int32_t group_top, int renormalize, float scale, float* weights,
+                 int32_t* experts, void* stream);
+int lapsum_route_backward(const void* logits, int dtype, int64_t ld, int64_t T, int64_t E,
+                          int32_t k, int score, int renormalize, float scale,
+                          const float* weights, const int32_t* experts, const float* dweights,
+                          void* dlogits, int64_t ld_out, void* stream);
+
+/*
+ * Rows to experts and back.  lapsum_expert_plan sorts N = T*k assignments
+ * (experts[i], i = t*k + j; a value outside [0, E) is a dropped one) by expert,
+ * stably: offsets (E + 1 entries) is each expert's first place and, last, the
+ * number of assignments that are not dropped; slots[i] the place of assignment i;
+ * order[place] = i.  Dropped ones come behind all others, so slots is a
+ * permutation of 0 .. N - 1.  1 <= E <= 1024, N < 2^31.  ws:
+ * lapsum_expert_plan_workspace_bytes(N, E) bytes, 256-byte aligned (0: bad sizes).
+ *
+ * The row calls take slots (T*k) and live = &offsets[E] from the plan; rows of H
+ * elements of `dtype`, x and dout with row stride ld, the others dense;
+ * 1 <= k <= 32.
+ *   lapsum_expert_gather:   xs[slots[t*k+j]] = x[t]; rows behind the last expert are 0.
+ *   lapsum_expert_combine:  out[t] = sum_j weights[t*k+j] y[slots[t*k+j]] over the
+ *     assignments that are not dropped, in fp32 in the order of j, rounded once;
+ *     weights NULL: ones, which makes it the gradient of lapsum_expert_gather.
+ *   lapsum_expert_combine_backward:  dy[slots[t*k+j]] = weights[t*k+j] dout[t] and
+ *     dweights[t*k+j] = dout[t] . y[slots[t*k+j]]; 0 for dropped assignments.
+ * A slot outside [0, N) is skipped.  No result depends on the order of execution.
+ */
+size_t lapsum_expert_plan_workspace_bytes(int64_t N, int64_t E);
+int lapsum_expert_plan(const int32_t* experts, int64_t N, int64_t E, int32_t* offsets,
+                       int32_t* slots, int32_t* order, void* ws, size_t ws_bytes, void* stream);
+int lapsum_expert_gather(const void* x, int dtype, int64_t ld, int64_t T, int32_t k, int64_t H,
+                         const int32_t* slots, const int32_t* live, void* xs, void* stream);
+int lapsum_expert_combine(const void* y, int dtype, int64_t T, int32_t k, int64_t H,
+                          const int32_t* slots, const int32_t* live, const float* weights,
+                          void* out, void* stream);
+int lapsum_expert_combine_backward(const void* dout, int dtype, int64_t ld, const void* y,
+                                   int64_t T, int32_t k, int64_t H, const int32_t* slots,
+                                   const int32_t* live, const float* weights, void* dy,
+                                   float* dweights, void* stream);
+
+/*
+ * Attention over a cache with accumulated weight.  Sq tokens of each of B
+ * sequences, Hq query heads in groups of G = Hq / Hkv that share a key/value head;
+ * caches of N rows of D elements (bf16 or fp16) per sequence and head, of which
+ * the first lengths[b] (device, clamped to [0, N]) are filled, the Sq tokens' own
+ * keys last: token i sees the keys before lengths[b] - Sq + i + 1.  With p the
+ * softmax of scale * q . k over the keys a query sees,
+ *     out[b, i, hq] = sum_j p_j v_j                       (dense, q's type)
+ *     score_out[b, h, j] = score_in[b, h, j] + sum of p_j over the Sq * G queries
+ * for j < lengths[b]; scores behind are neither read nor written.  score_in NULL
+ * reads as 0; it may be score_out itself (else they must not overlap).  A query
+ * that sees no key gets out = 0 and adds nothing.  Cache rows behind lengths[b] may
+ * hold anything.  `strides` (host, 13 entries, in elements): batch, head and token
+ * stride of q; batch, head and row stride of k, then of v; batch and head stride
+ * of score_in, then of score_out (the elements of a row, and a head's scores, are
+ * consecutive).  D is a multiple of 16 up to 256; q, k, v and out are 16-byte
+ * aligned and their strides multiples of 8; Hq a multiple of Hkv.  Softmax
+ * statistics, sums and scores are fp32.  ws: lapsum_attend_workspace_bytes(...)
+ * bytes, 256-byte aligned (0: bad sizes).
+ */
+size_t lapsum_attend_workspace_bytes(int64_t B, int64_t Sq, int64_t Hq, int64_t Hkv, int64_t N,
+                                     int64_t D);
+int lapsum_attend_accumulate(const void* q, const void* k, const void* v, int dtype,
+                             const int32_t* lengths, const int64_t* strides, int64_t B,
+                             int64_t Sq, int64_t Hq, int64_t Hkv, int64_t N, int64_t D,
+                             float scale, const float* score_in, float* score_out, void* out,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Eviction by accumulated weight.  For each of B sequences and H heads, of the
+ * first n = lengths[b] (device, clamped to [0, N]) cache rows min(n, budget) stay:
+ * the first `first`, the last `last`, and the largest scores of those between
+ * (equal scores: the lower position; NaN below every number), in ascending order
+ * of position.  k_out, v_out, score_out get their rows and scores at 0, 1, ...,
+ * positions (B*H*budget, dense) their positions and lengths_out[b] = min(n,
+ * budget); between min(n, budget) and budget the outputs are 0 (positions -1), and
+ * cache rows from `budget` on are left as they were.  Rows are D elements of
+ * `dtype`.  `strides` (host, 16 entries, in elements): batch, head and row stride
+ * of k, then of v; batch and head stride of score; the same eight of k_out,
+ * v_out and score_out.  The outputs must not overlap the inputs.  first + last <= budget.
+ */
+int lapsum_evict(const void* k, const void* v, int dtype, const float* score,
+                 const int32_t* lengths, const int64_t* strides, int64_t B, int64_t H, int64_t N,
+                 int64_t D, int64_t budget, int64_t first, int64_t last, void* k_out, void* v_out,
+                 float* score_out, int32_t* positions, int32_t* lengths_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -27,7 +27,9 @@ __all__ = [
     "LapSumError", "Workspace", "forward", "backward", "read_status", "row_info", "sample_values",
     "workspace_bytes", "soft_topk", "LapSumTopK", "PATHS", "FLAG_FORCE_MISS", "FLAG_NO_RETRY",
     "FLAG_ONE_CTA_SOLVE", "library_path", "profile_enable", "backward_kt", "profile_read", "backward_noalloc", "Support",
-    "support_bytes", "forward_lowp", "backward_lowp",
+    "support_bytes", "forward_lowp", "backward_lowp", "route_experts", "route_backward",
+    "ExpertPlan", "expert_plan", "expert_gather", "expert_combine", "attend_accumulate", "evict",
+    "Evicted",
 ]
 
 PATHS = {"auto": 0, "fullsort": 1, "bracket": 2, "radix": 3, "rowbracket": 4}
@@ -147,6 +149,38 @@ def _lib():
         lib.lapsum_backward_lowp.argtypes = [_vp, ctypes.c_int, _c_i64, _vp, _vp, _vp, _c_i64,
                                              _c_i64, ctypes.c_double, _vp, ctypes.c_size_t, _vp,
                                              ctypes.c_size_t, _vp]
+        i32, f32, i64s = ctypes.c_int32, ctypes.c_float, ctypes.POINTER(_c_i64)
+        lib.lapsum_route.restype = ctypes.c_int
+        lib.lapsum_route.argtypes = [_vp, ctypes.c_int, _c_i64, _c_i64, _c_i64, i32, ctypes.c_int,
+                                     _vp, i32, i32, i32, ctypes.c_int, f32, _vp, _vp, _vp]
+        lib.lapsum_route_backward.restype = ctypes.c_int
+        lib.lapsum_route_backward.argtypes = [_vp, ctypes.c_int, _c_i64, _c_i64, _c_i64, i32,
+                                              ctypes.c_int, ctypes.c_int, f32, _vp, _vp, _vp, _vp,
+                                              _c_i64, _vp]
+        lib.lapsum_expert_plan_workspace_bytes.restype = ctypes.c_size_t
+        lib.lapsum_expert_plan_workspace_bytes.argtypes = [_c_i64, _c_i64]
+        lib.lapsum_expert_plan.restype = ctypes.c_int
+        lib.lapsum_expert_plan.argtypes = [_vp, _c_i64, _c_i64, _vp, _vp, _vp, _vp,
+                                           ctypes.c_size_t, _vp]
+        lib.lapsum_expert_gather.restype = ctypes.c_int
+        lib.lapsum_expert_gather.argtypes = [_vp, ctypes.c_int, _c_i64, _c_i64, i32, _c_i64, _vp,
+                                             _vp, _vp, _vp]
+        lib.lapsum_expert_combine.restype = ctypes.c_int
+        lib.lapsum_expert_combine.argtypes = [_vp, ctypes.c_int, _c_i64, i32, _c_i64, _vp, _vp,
+                                              _vp, _vp, _vp]
+        lib.lapsum_expert_combine_backward.restype = ctypes.c_int
+        lib.lapsum_expert_combine_backward.argtypes = [_vp, ctypes.c_int, _c_i64, _vp, _c_i64, i32,
+                                                       _c_i64, _vp, _vp, _vp, _vp, _vp, _vp]
+        lib.lapsum_attend_workspace_bytes.restype = ctypes.c_size_t
+        lib.lapsum_attend_workspace_bytes.argtypes = [_c_i64] * 6
+        lib.lapsum_attend_accumulate.restype = ctypes.c_int
+        lib.lapsum_attend_accumulate.argtypes = [_vp, _vp, _vp, ctypes.c_int, _vp, i64s, _c_i64,
+                                                 _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, f32, _vp,
+                                                 _vp, _vp, _vp, ctypes.c_size_t, _vp]
+        lib.lapsum_evict.restype = ctypes.c_int
+        lib.lapsum_evict.argtypes = [_vp, _vp, ctypes.c_int, _vp, _vp, i64s, _c_i64, _c_i64,
+                                     _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _vp,
+                                     _vp, _vp]
         _LIB = lib
     return _LIB
 
@@ -676,3 +710,8 @@ def soft_topk(r: torch.Tensor, k, t: float, path="auto", seed: int = 0) -> torch
     """Differentiable soft top-k probabilities p with sum p = k per row (k a number,
     or a 1-D tensor with one budget per row)."""
     return LapSumTopK.apply(r, k, t, path, seed)
+
+
+from .cache import Evicted, attend_accumulate, evict  # noqa: E402
+from .experts import (ExpertPlan, expert_combine, expert_gather, expert_plan,  # noqa: E402
+                      route_backward, route_experts)

@@ -1,0 +1,148 @@
+"""A cache that is pruned by the weight its keys received: ``attend_accumulate``
+(attention over the cache that adds each key's weight to a score) and ``evict``
+(the keys with the largest scores, gathered in order).
+
+The definitions stand in ``include/lapsum.h``; memory selection is one of the
+uses the pages of "Fast LapSum: Exact Differentiable Top-k at Million Scale"
+name (gist.science explainer pages, section 4.2).
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from . import _lib
+from ._launch import DTYPES, distinct, extent, launch, need, overlap
+
+_HALF = (torch.bfloat16, torch.float16)
+
+
+def _check_caches(k, v, score, lengths, dtypes):
+    need(k, "k", dtypes, 4)
+    need(v, "v", (k.dtype,), 4, k.device)
+    need(score, "score", (torch.float32,), 3, k.device)
+    need(lengths, "lengths", (torch.int32,), 1, k.device)
+    if v.shape != k.shape or score.shape != k.shape[:3] or lengths.shape[0] != k.shape[0]:
+        raise ValueError("k and v must be (B, H, N, D), score (B, H, N) and lengths (B)")
+    for x, name in ((k, "k"), (v, "v"), (score, "score")):
+        if x.shape[-1] > 1 and x.stride(-1) != 1:
+            raise ValueError(f"{name} must be consecutive in its last dimension")
+    if not lengths.is_contiguous():
+        raise ValueError("lengths must be contiguous")
+
+
+def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths: torch.Tensor,
+                      score: torch.Tensor, *, scale: float = None, score_out: torch.Tensor = None,
+                      out: torch.Tensor = None) -> torch.Tensor:
+    """Attention of q (B, Sq, Hq, D) over caches k, v (B, Hkv, N, D), bfloat16 or
+    float16, filled up to ``lengths`` (B, int32) with the Sq tokens' own keys last;
+    returns (B, Sq, Hq, D).  ``score`` (B, Hkv, N, float32) grows in place by the weight
+    that each key received from the Sq * Hq / Hkv queries of its head, or
+    ``score_out`` gets the sum and ``score`` stays.
+
+    A token i sees the keys before lengths - Sq + i + 1; one that sees none gets 0.
+    ``scale`` is D ** -0.5 by default.  D is a multiple of 16 up to 256; the tensors may
+    be strided views whose rows start on 16 bytes.  No gradient."""
+    _check_caches(k, v, score, lengths, _HALF)
+    need(q, "q", (k.dtype,), 4, k.device)
+    B, Sq, Hq, D = q.shape
+    Hkv, N = k.shape[1], k.shape[2]
+    if B != k.shape[0] or D != k.shape[3] or Hkv < 1 or Hq % Hkv != 0:
+        raise ValueError("q must be (B, Sq, Hq, D) with Hq a multiple of the caches' heads")
+    if D > 1 and q.stride(3) != 1:
+        raise ValueError("q must be consecutive in its last dimension")
+    if score_out is None:
+        score_out = score
+    else:
+        need(score_out, "score_out", (torch.float32,), 3, k.device)
+        if score_out.shape != score.shape or N > 1 and score_out.stride(2) != 1:
+            raise ValueError("score_out must have score's shape, consecutive in its last dimension")
+        same = score_out.data_ptr() == score.data_ptr() and score_out.stride() == score.stride()
+        if not same and overlap(score, score_out):
+            raise ValueError("score_out must be score itself or not overlap it")
+    if not distinct(score_out):
+        raise ValueError("the scores written must not share memory")
+    if out is None:
+        out = torch.empty((B, Sq, Hq, D), dtype=q.dtype, device=q.device)
+    else:
+        need(out, "out", (q.dtype,), 4, q.device)
+        if out.shape != q.shape or not out.is_contiguous():
+            raise ValueError("out must be contiguous and have q's shape")
+        if any(overlap(out, x) for x in (q, k, v, score, score_out)):
+            raise ValueError("out must not overlap the inputs")
+    if out.numel() == 0:
+        if score_out is not score and B * Hkv * N > 0:
+            raise ValueError("nothing to attend with: Sq is 0")
+        return out
+    if N == 0:
+        return out.zero_()
+    strides = (ctypes.c_int64 * 13)(q.stride(0), q.stride(2), q.stride(1), *k.stride()[:3],
+                                    *v.stride()[:3], *score.stride()[:2], *score_out.stride()[:2])
+    lib = _lib()
+    nbytes = lib.lapsum_attend_workspace_bytes(B, Sq, Hq, Hkv, N, D)
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
+    launch(lib.lapsum_attend_accumulate, q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+           DTYPES[q.dtype], lengths.data_ptr(), strides, B, Sq, Hq, Hkv, N, D,
+           D ** -0.5 if scale is None else float(scale), score.data_ptr(), score_out.data_ptr(),
+           out.data_ptr(), ws.data_ptr(), nbytes)
+    return out
+
+
+class Evicted(NamedTuple):
+    """The caches and scores that stayed, their positions before (-1: none) and the
+    new lengths."""
+    k: torch.Tensor
+    v: torch.Tensor
+    score: torch.Tensor
+    positions: torch.Tensor
+    lengths: torch.Tensor
+
+
+def evict(k: torch.Tensor, v: torch.Tensor, score: torch.Tensor, lengths: torch.Tensor,
+          budget: int, *, first: int = 0, last: int = 0, out=None) -> Evicted:
+    """Keeps ``budget`` of the first ``lengths`` (B, int32) rows of caches k, v
+    (B, H, N, D; float32, bfloat16 or float16) per sequence and head: the first
+    ``first``, the last ``last``, and those between with the largest ``score``
+    (B, H, N, float32; ties: the lower position), in the order of their positions.
+
+    ``out`` may hold the caches and scores to fill, (k, v, score) with at least
+    ``budget`` rows; rows from ``budget`` on are left as they were.  Rows that no key
+    fills (fewer than ``budget`` in the cache) are 0 and their positions -1."""
+    _check_caches(k, v, score, lengths, DTYPES)
+    B, H, N, D = k.shape
+    budget, first, last = int(budget), int(first), int(last)
+    if budget < 1 or first < 0 or last < 0 or first + last > budget:
+        raise ValueError("budget must be at least 1, and first + last at most budget")
+    if out is None:
+        ko = torch.empty((B, H, budget, D), dtype=k.dtype, device=k.device)
+        vo = torch.empty_like(ko)
+        so = torch.empty((B, H, budget), dtype=torch.float32, device=k.device)
+    else:
+        ko, vo, so = out
+        need(ko, "out[0]", (k.dtype,), 4, k.device)
+        need(vo, "out[1]", (k.dtype,), 4, k.device)
+        need(so, "out[2]", (torch.float32,), 3, k.device)
+        for x, d in ((ko, (D,)), (vo, (D,)), (so, ())):
+            if x.shape[:2] != (B, H) or x.shape[2] < budget or tuple(x.shape[3:]) != d or \
+                    x.shape[-1] > 1 and x.stride(-1) != 1 or not distinct(x):
+                raise ValueError("out must be (B, H, C, D), (B, H, C, D) and (B, H, C) with "
+                                 "C >= budget, consecutive in the last dimension")
+        if any(overlap(x, y) for x in (ko, vo, so) for y in (k, v, score, lengths)) or \
+                extent(ko) == extent(vo):
+            raise ValueError("out must not overlap the inputs")
+    positions = torch.empty((B, H, budget), dtype=torch.int32, device=k.device)
+    left = torch.empty(B, dtype=torch.int32, device=k.device)
+    result = Evicted(ko, vo, so, positions, left)
+    if B * H * D == 0 or N == 0:
+        if B * H > 0:
+            raise ValueError("the caches must hold at least one row of one element")
+        left.copy_(lengths.clamp(0, min(N, budget)))
+        return result
+    strides = (ctypes.c_int64 * 16)(*k.stride()[:3], *v.stride()[:3], *score.stride()[:2],
+                                    *ko.stride()[:3], *vo.stride()[:3], *so.stride()[:2])
+    launch(_lib().lapsum_evict, k.device, k.data_ptr(), v.data_ptr(), DTYPES[k.dtype],
+           score.data_ptr(), lengths.data_ptr(), strides, B, H, N, D, budget, first, last,
+           ko.data_ptr(), vo.data_ptr(), so.data_ptr(), positions.data_ptr(), left.data_ptr())
+    return result

@@ -1,0 +1,562 @@
+// Expert routing: the hard top-k of a mixture-of-experts router, its weights
+// and the gradient of its logits.  Entry points: lapsum_route and
+// lapsum_route_backward (include/lapsum.h).
+//
+// One warp holds one row of E <= 1024 logits in registers, lane l the
+// consecutive experts [l V, (l + 1) V), V = E/32 rounded up to a power of two,
+// so that "lowest index first" is "lowest lane first, then lowest slot".  The k
+// largest keys come out one by one: a warp-wide integer maximum of the lanes'
+// best keys, a ballot for the lane that holds it, and that lane looks up its
+// next best.
+//
+// Keys.  Without a bias and groups, the scores rise strictly with the logits,
+// so the logits themselves are the keys and the order is exact.  With a bias (or for
+// the groups' sums) keys are formed in fp32 with a bound on their error, and a
+// row in which two neighbouring ranks lie nearer than that bound is done again
+// with fp64 keys, so that the choice is always that of the fp64 keys; that is
+// rare unless the keys really are equal.
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "elements.cuh"
+#include "lapsum_common.cuh"
+#include "lapsum_kernels.h"
+
+namespace lapsum {
+namespace {
+
+constexpr int kRouteMaxE = 1024;
+constexpr int kRouteMaxK = 32;
+constexpr int kRouteMaxG = 32;
+constexpr int kRouteWarps = 4;
+constexpr unsigned kAll = 0xffffffffu;
+
+struct RouteArgs {
+    int64_t ld, T;
+    int E, k;
+    int sigmoid;
+    const float* bias;
+    int groups, top_groups, group_top;
+    int renorm;
+    float scale;
+    int vec;
+    int scratch;  // doubles of shared memory per warp
+};
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, d));
+    return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
+    return x;
+}
+
+// This lane's V logits of a row; experts past E read as -inf.
+template <class T, int V>
+__device__ __forceinline__ void load_lane(const T* row, int E, int lane, bool vec, float out[V]) {
+    constexpr int W = V * (int)sizeof(T) <= 16 ? V : 16 / (int)sizeof(T);
+    const int base = lane * V;
+#pragma unroll
+    for (int i = 0; i < V; i += W) {
+        if (vec && base + i + W <= E) {
+            const Pack<T, W> p = *reinterpret_cast<const Pack<T, W>*>(row + base + i);
+#pragma unroll
+            for (int j = 0; j < W; ++j) out[i + j] = widen(p.v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                out[i + j] = base + i + j < E ? widen(row[base + i + j]) : -INFINITY;
+        }
+    }
+}
+
+__device__ __forceinline__ float sigmoid_f(float l) { return 1.f / (1.f + expf(-l)); }
+
+// Where expert e of a row lies in the warp's scratch (padded against bank conflicts).
+__device__ __forceinline__ int pad_slot(int e) { return e + (e >> 5); }
+int pad_size(int E) { return E + (E >> 5) + 1; }
+
+// Key of a group: the sum of its 1 or 2 largest keys; -inf when it has none.  The
+// lanes of one group (`sub` consecutive ones) share its experts.
+template <class F>
+__device__ __forceinline__ F group_score(const F* keys, int size, int g, int groups, int j, int sub,
+                                         int group_top) {
+    F a = (F)-INFINITY, b = (F)-INFINITY;
+    if (g < groups)
+        for (int i = j; i < size; i += sub) {
+            const F x = keys[pad_slot(g * size + i)];
+            if (x > a) {
+                b = a;
+                a = x;
+            } else if (x > b) {
+                b = x;
+            }
+        }
+    for (int d = 1; d < sub; d <<= 1) {
+        const F a2 = __shfl_xor_sync(kAll, a, d), b2 = __shfl_xor_sync(kAll, b, d);
+        const F lo = a < a2 ? a : a2, hi = a < a2 ? a2 : a;
+        const F m = b < b2 ? b2 : b;
+        a = hi;
+        b = lo < m ? m : lo;
+    }
+    return group_top == 2 && b > (F)-INFINITY ? a + b : a;
+}
+
+// The groups that are kept, as a bit mask: rank each group among all by (score,
+// lowest index).  `gap` (when not null) gets the distance between the last kept
+// and the first dropped score that are not both -inf.
+template <class F>
+__device__ __forceinline__ unsigned kept_groups(F mine, int g, int groups, int sub, int top,
+                                                F* gap) {
+    int rank = 0;
+    for (int o = 0; o < groups; ++o) {
+        const F x = __shfl_sync(kAll, mine, o * sub);
+        if (x > mine || (x == mine && o < g)) ++rank;
+    }
+    const bool real = g < groups && mine > (F)-INFINITY;
+    const bool keep = real && rank < top;
+    unsigned mask = 0;
+    for (int o = 0; o < groups; ++o)
+        mask |= (__shfl_sync(kAll, keep ? 1u : 0u, o * sub)) << o;
+    if (gap != nullptr) {
+        F lo = keep ? mine : (F)INFINITY, hi = real && !keep ? mine : (F)-INFINITY;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            const F l2 = __shfl_xor_sync(kAll, lo, d), h2 = __shfl_xor_sync(kAll, hi, d);
+            lo = l2 < lo ? l2 : lo;
+            hi = h2 > hi ? h2 : hi;
+        }
+        *gap = hi > (F)-INFINITY && lo < (F)INFINITY ? lo - hi : (F)INFINITY;
+    }
+    return mask;
+}
+
+// The choice with fp64 keys, from the logits in memory: the j-th chosen expert
+// is returned on lane j (-1: none).  `keys` is the warp's scratch.
+template <class T>
+__device__ __noinline__ int route_row_fp64(const T* row, const RouteArgs& a, int lane,
+                                           double* keys) {
+    double m = -INFINITY;
+    for (int e = lane; e < a.E; e += 32) m = fmax(m, (double)widen(row[e]));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmax(m, __shfl_xor_sync(kAll, m, d));
+    double total = 0.0;
+    if (!a.sigmoid) {
+        for (int e = lane; e < a.E; e += 32) total += exp((double)widen(row[e]) - m);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
+    }
+    __syncwarp();
+    for (int e = lane; e < a.E; e += 32) {
+        const double l = (double)widen(row[e]);
+        double c = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / total;
+        if (a.bias != nullptr) c += (double)a.bias[e];
+        keys[pad_slot(e)] = l == -INFINITY ? -INFINITY : c;
+    }
+    __syncwarp();
+    unsigned kept = kAll;
+    const int size = a.E / a.groups;
+    if (a.groups > 1) {
+        int gp = 1;
+        while (gp < a.groups) gp <<= 1;
+        const int sub = 32 / gp, g = lane / sub;
+        const double mine =
+            group_score<double>(keys, size, g, a.groups, lane % sub, sub, a.group_top);
+        kept = kept_groups<double>(mine, g, a.groups, sub, a.top_groups, nullptr);
+    }
+    int chosen = -1;
+    for (int j = 0; j < a.k; ++j) {
+        double best = -INFINITY;
+        int at = a.E;
+        for (int e = lane; e < a.E; e += 32)
+            if ((kept >> (a.groups > 1 ? e / size : 0)) & 1u) {
+                const double x = keys[pad_slot(e)];
+                // without a bias the logits break ties of keys that round to the same
+                const bool better =
+                    x > best || (x == best && at < a.E && a.bias == nullptr &&
+                                 widen(row[e]) > widen(row[at]));
+                if (better) {
+                    best = x;
+                    at = e;
+                }
+            }
+        float lb = at < a.E ? widen(row[at]) : -INFINITY;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) {
+            const double x = __shfl_xor_sync(kAll, best, d);
+            const int o = __shfl_xor_sync(kAll, at, d);
+            const float lo = __shfl_xor_sync(kAll, lb, d);
+            const bool up = a.bias == nullptr && lo != lb ? lo > lb : o < at;
+            if (x > best || (x == best && up)) {
+                best = x;
+                at = o;
+                lb = lo;
+            }
+        }
+        if (!(best > -INFINITY)) break;
+        if (lane == j) chosen = at;
+        __syncwarp();
+        if (lane == 0) keys[pad_slot(at)] = -INFINITY;
+        __syncwarp();
+    }
+    return chosen;
+}
+
+// One warp per row.  kKeyed: keys are scores (+ bias) or groups limit the
+// choice; otherwise the logits are the keys.
+template <class T, int V, bool kKeyed>
+__global__ void __launch_bounds__(kRouteWarps * 32)
+    route_kernel(const T* logits, RouteArgs a, float* weights, int32_t* experts) {
+    pdl_wait();
+    extern __shared__ double route_scratch[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+    if (t >= a.T) return;
+    const T* row = logits + t * a.ld;
+    float l[V];
+    load_lane<T, V>(row, a.E, lane, a.vec != 0, l);
+
+    float m = -INFINITY;
+    bool bad = false;  // a NaN or +inf anywhere makes the row's answer NaN
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        bad |= !(l[i] < INFINITY);
+        m = fmaxf(m, l[i]);
+    }
+    m = warp_max(m);
+
+    float total = 0.f;  // softmax: the sum of e^{l - m} over all experts
+    if (!a.sigmoid && (kKeyed || !a.renorm)) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) s += l[i] == -INFINITY ? 0.f : expf(l[i] - m);
+        total = warp_sum(s);
+    }
+
+    uint32_t key[V];  // 0: not to be chosen (no finite value has that key)
+    bool near = false;
+    float tol = 0.f;
+    if constexpr (kKeyed) {
+        float* fs = reinterpret_cast<float*>(route_scratch + (size_t)warp * a.scratch);
+        const float inv = total > 0.f ? 1.f / total : 0.f;
+        float c[V];
+        float cmax = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane * V + i;
+            c[i] = -INFINITY;
+            if (l[i] > -INFINITY) {
+                float x = a.sigmoid ? sigmoid_f(l[i]) : expf(l[i] - m) * inv;
+                if (a.bias != nullptr) x += a.bias[e];
+                bad |= !(x < INFINITY);
+                c[i] = x;
+                if (x > -INFINITY) cmax = fmaxf(cmax, fabsf(x));
+            }
+        }
+        // The scores' error is a few units of 2^-24 of the largest one (sigmoid:
+        // of 1; softmax: e^{l-m} carries |l - m| 2^-24 relative, and x e^{-x} < 1),
+        // the sum's 2^-24 of the key; 2^-20 of both together leaves room.
+        cmax = warp_max(cmax);
+        tol = 9.5e-7f * (cmax + (a.sigmoid ? 1.f : inv));
+        unsigned kept = kAll;
+        const int size = a.E / a.groups;
+        if (a.groups > 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (lane * V + i < a.E) fs[pad_slot(lane * V + i)] = c[i];
+            __syncwarp();
+            int gp = 1;
+            while (gp < a.groups) gp <<= 1;
+            const int sub = 32 / gp, g = lane / sub;
+            const float mine =
+                group_score<float>(fs, size, g, a.groups, lane % sub, sub, a.group_top);
+            float gap;
+            kept = kept_groups<float>(mine, g, a.groups, sub, a.top_groups, &gap);
+            near |= gap <= 4.f * tol;
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane * V + i;
+            const bool in = c[i] > -INFINITY && (a.groups == 1 || ((kept >> (e / size)) & 1u));
+            // -0 and +0 are one value
+            key[i] = in ? to_key((a.bias != nullptr ? c[i] : l[i]) + 0.f) : 0u;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = l[i] > -INFINITY ? to_key(l[i] + 0.f) : 0u;
+    }
+    bad = __any_sync(kAll, bad);
+
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) best = key[i] > best ? key[i] : best;
+    int chosen = -1;
+    uint32_t last = 0;
+    // with a bias one rank more is looked at: the chosen set ends between two keys
+    const bool check = kKeyed && a.bias != nullptr;
+    const int rounds = a.k + (check ? 1 : 0);
+    for (int j = 0; j < rounds; ++j) {
+        const uint32_t top = __reduce_max_sync(kAll, best);
+        if (top == 0u) break;
+        if (check) {
+            near |= j > 0 && from_key(last) - from_key(top) <= 2.f * tol;
+            last = top;
+        }
+        const unsigned holders = __ballot_sync(kAll, best == top);
+        const int src = __ffs(holders) - 1;
+        int at = 0;
+        if (lane == src) {
+            bool found = false;
+            best = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (!found && key[i] == top) {
+                    found = true;
+                    at = lane * V + i;
+                    key[i] = 0;
+                }
+                best = key[i] > best ? key[i] : best;
+            }
+        }
+        at = __shfl_sync(kAll, at, src);
+        if (lane == j) chosen = at;  // the extra round's lane k keeps nothing: k < 32 or no lane
+    }
+    if (lane >= a.k) chosen = -1;
+    if constexpr (kKeyed) {
+        if (near && !bad)
+            chosen = route_row_fp64<T>(row, a, lane, route_scratch + (size_t)warp * a.scratch);
+    }
+
+    // weights: lane j owns the j-th choice
+    float w = 0.f;
+    const float lc = chosen >= 0 ? widen(row[chosen]) : -INFINITY;
+    if (a.renorm) {
+        const float lm = warp_max(lc);
+        // softmax: the sum over all experts cancels, leaving a softmax over the
+        // chosen ones.  Sigmoids that are all below e^-60 equal e^l to fp32, so
+        // the same form keeps their ratio where they would underflow.
+        const bool expform = !a.sigmoid || lm < -60.f;
+        const float s = chosen < 0 ? 0.f : expform ? expf(lc - lm) : sigmoid_f(lc);
+        const float sum = warp_sum(s);
+        w = chosen < 0 ? 0.f : s / sum * a.scale;
+    } else if (chosen >= 0) {
+        w = (a.sigmoid ? sigmoid_f(lc) : expf(lc - m) / total) * a.scale;
+    }
+    if (bad) {
+        chosen = -1;
+        w = NAN;
+    }
+    if (lane < a.k) {
+        weights[t * a.k + lane] = w;
+        experts[t * a.k + lane] = chosen;
+    }
+}
+
+// Gradient of the logits.  With s the scores, w the weights and u = dL/dw:
+//   renormalised: d_i = w_i (u_i - sum_j u_j w_j / scale) on the chosen experts
+//                 (softmax), times 1 - s_i (sigmoid), 0 elsewhere;
+//   softmax:      d_i = s_i (scale u_i [i chosen] - sum_j u_j w_j) on all experts;
+//   sigmoid:      d_i = u_i w_i (1 - s_i) on the chosen experts.
+// A row whose weights are NaN gets NaN.
+template <class T, int V>
+__global__ void __launch_bounds__(kRouteWarps * 32)
+    route_backward_kernel(const T* logits, RouteArgs a, const float* weights,
+                          const int32_t* experts, const float* dw, T* out, int64_t ld_out,
+                          int vec_out) {
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
+    if (t >= a.T) return;
+    const T* row = logits + t * a.ld;
+    int e = -1;
+    float w = 0.f, u = 0.f;
+    bool bad = false;
+    if (lane < a.k) {
+        e = experts[t * a.k + lane];
+        w = weights[t * a.k + lane];
+        bad = isnan(w);
+        if (e >= a.E) e = -1;
+        if (e >= 0) u = dw[t * a.k + lane];
+    }
+    bad = __any_sync(kAll, bad);
+    const float dot = warp_sum(e >= 0 ? u * w : 0.f);
+    float own = 0.f;  // this lane's chosen expert: its gradient, or (plain softmax) scale u
+    const bool dense = !a.sigmoid && !a.renorm;
+    if (e >= 0) {
+        if (dense) own = a.scale * u;
+        else {
+            own = w * (a.renorm ? u - dot / a.scale : u);
+            if (a.sigmoid) own *= sigmoid_f(-widen(row[e]));  // 1 - s
+        }
+    }
+    float d[V];
+    if (dense) {
+        float l[V];
+        load_lane<T, V>(row, a.E, lane, a.vec != 0, l);
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+        m = warp_max(m);
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            l[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - m);
+            s += l[i];
+        }
+        s = warp_sum(s);
+        const float inv = s > 0.f ? 1.f / s : 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = l[i] * inv;
+        float g[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) g[i] = -dot;
+        for (int j = 0; j < a.k; ++j) {
+            const int ej = __shfl_sync(kAll, e, j) - lane * V;
+            const float gj = __shfl_sync(kAll, own, j);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (ej == i) g[i] += gj;
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = d[i] == 0.f ? 0.f : d[i] * g[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = 0.f;
+        for (int j = 0; j < a.k; ++j) {
+            const int ej = __shfl_sync(kAll, e, j) - lane * V;
+            const float gj = __shfl_sync(kAll, own, j);
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (ej == i) d[i] += gj;
+        }
+    }
+    if (bad) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = NAN;
+    }
+    constexpr int W = V * (int)sizeof(T) <= 16 ? V : 16 / (int)sizeof(T);
+    T* o = out + t * ld_out;
+    const int base = lane * V;
+#pragma unroll
+    for (int i = 0; i < V; i += W) {
+        if (vec_out && base + i + W <= a.E) {
+            Pack<T, W> p;
+#pragma unroll
+            for (int j = 0; j < W; ++j) p.v[j] = narrow<T>(d[i + j]);
+            *reinterpret_cast<Pack<T, W>*>(o + base + i) = p;
+        } else {
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                if (base + i + j < a.E) o[base + i + j] = narrow<T>(d[i + j]);
+        }
+    }
+}
+
+int lane_values(int E) {
+    int v = 1;
+    while (v * 32 < E) v <<= 1;
+    return v;
+}
+
+template <class F>
+cudaError_t with_lane_values(int E, F f) {
+    switch (lane_values(E)) {
+        case 1: return f(std::integral_constant<int, 1>{});
+        case 2: return f(std::integral_constant<int, 2>{});
+        case 4: return f(std::integral_constant<int, 4>{});
+        case 8: return f(std::integral_constant<int, 8>{});
+        case 16: return f(std::integral_constant<int, 16>{});
+        default: return f(std::integral_constant<int, 32>{});
+    }
+}
+
+// Whether a lane's V elements can be moved as 16-byte (or shorter) packs.
+bool lane_packs(const void* p, int64_t ld, int E, int size) {
+    const int v = lane_values(E), w = v * size <= 16 ? v : 16 / size;
+    return aligned_to(p, (size_t)w * size) && ld % w == 0;
+}
+
+bool route_sizes_ok(int64_t ld, int64_t T, int64_t E, int32_t k, int score, float scale) {
+    return T >= 1 && T <= (int64_t(1) << 31) && E >= 1 && E <= kRouteMaxE && k >= 1 &&
+           k <= kRouteMaxK && k <= E && ld >= E &&
+           (score == LAPSUM_SCORE_SOFTMAX || score == LAPSUM_SCORE_SIGMOID) && scale > 0.f &&
+           std::isfinite(scale);
+}
+
+}  // namespace
+}  // namespace lapsum
+
+using namespace lapsum;
+
+extern "C" int lapsum_route(const void* logits, int dtype, int64_t ld, int64_t T, int64_t E,
+                            int32_t k, int score, const float* bias, int32_t groups,
+                            int32_t top_groups, int32_t group_top, int renormalize, float scale,
+                            float* weights, int32_t* experts, void* stream) {
+    if (logits == nullptr || weights == nullptr || experts == nullptr) return LAPSUM_EINVAL;
+    if (!known_dtype(dtype) || !route_sizes_ok(ld, T, E, k, score, scale)) return LAPSUM_EINVAL;
+    if (groups < 1 || groups > kRouteMaxG || E % groups != 0 || top_groups < 1 ||
+        top_groups > groups || (group_top != 1 && group_top != 2))
+        return LAPSUM_EINVAL;
+    if (k > top_groups * (E / groups)) return LAPSUM_EINVAL;
+    if (!aligned_to(logits, dtype_size(dtype)) || !aligned_to(weights, 4) ||
+        !aligned_to(experts, 4) || !aligned_to(bias, 4))
+        return LAPSUM_EINVAL;
+    // keeping every group limits nothing
+    const int g = top_groups == groups ? 1 : groups;
+    RouteArgs a{ld, T, (int)E, k, score == LAPSUM_SCORE_SIGMOID, bias, g, g == 1 ? 1 : top_groups,
+                group_top, renormalize != 0, scale,
+                lane_packs(logits, ld, (int)E, dtype_size(dtype)) ? 1 : 0,
+                pad_size((int)E)};
+    cudaStream_t st = (cudaStream_t)stream;
+    const dim3 grid((unsigned)((T + kRouteWarps - 1) / kRouteWarps)), block(kRouteWarps * 32);
+    ProfScope prof("route", st);
+    const cudaError_t e = with_dtype(dtype, [&](auto* tag) {
+        using T_ = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
+        return with_lane_values((int)E, [&](auto v) {
+            constexpr int V = decltype(v)::value;
+            if (bias != nullptr || g > 1)
+                return launch_pdl(route_kernel<T_, V, true>, grid, block,
+                                  (size_t)kRouteWarps * a.scratch * sizeof(double), st,
+                                  (const T_*)logits, a, weights, experts);
+            return launch_pdl(route_kernel<T_, V, false>, grid, block, 0, st, (const T_*)logits, a,
+                              weights, experts);
+        });
+    });
+    return e == cudaSuccess ? LAPSUM_OK : LAPSUM_ECUDA;
+}
+
+extern "C" int lapsum_route_backward(const void* logits, int dtype, int64_t ld, int64_t T,
+                                     int64_t E, int32_t k, int score, int renormalize, float scale,
+                                     const float* weights, const int32_t* experts,
+                                     const float* dweights, void* dlogits, int64_t ld_out,
+                                     void* stream) {
+    if (logits == nullptr || weights == nullptr || experts == nullptr || dweights == nullptr ||
+        dlogits == nullptr)
+        return LAPSUM_EINVAL;
+    if (!known_dtype(dtype) || !route_sizes_ok(ld, T, E, k, score, scale) || ld_out < E)
+        return LAPSUM_EINVAL;
+    const int size = dtype_size(dtype);
+    if (!aligned_to(logits, size) || !aligned_to(dlogits, size) || !aligned_to(weights, 4) ||
+        !aligned_to(experts, 4) || !aligned_to(dweights, 4))
+        return LAPSUM_EINVAL;
+    RouteArgs a{ld, T, (int)E, k, score == LAPSUM_SCORE_SIGMOID, nullptr, 1, 1, 1,
+                renormalize != 0, scale, lane_packs(logits, ld, (int)E, size) ? 1 : 0, 0};
+    const int vec_out = lane_packs(dlogits, ld_out, (int)E, size) ? 1 : 0;
+    cudaStream_t st = (cudaStream_t)stream;
+    const dim3 grid((unsigned)((T + kRouteWarps - 1) / kRouteWarps)), block(kRouteWarps * 32);
+    ProfScope prof("route_backward", st);
+    const cudaError_t e = with_dtype(dtype, [&](auto* tag) {
+        using T_ = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
+        return with_lane_values((int)E, [&](auto v) {
+            constexpr int V = decltype(v)::value;
+            return launch_pdl(route_backward_kernel<T_, V>, grid, block, 0, st, (const T_*)logits,
+                              a, weights, experts, dweights, (T_*)dlogits, ld_out, vec_out);
+        });
+    });
+    return e == cudaSuccess ? LAPSUM_OK : LAPSUM_ECUDA;
+}

@@ -1,0 +1,361 @@
+"""Cache attention with accumulated weight, and eviction, against 64-bit plain forms.
+
+Tolerances, counted in roundings.  A logit is a sum of D products of 16-bit values,
+exact in fp32 and added in fp32: off by at most D 2^-24 of the sum of their
+magnitudes, times the scale, and the softmax's exponent by that and a rounding of
+its own argument; a weight's relative error is the sum of those (plus the sum of N
+weights, all of one sign).  The output takes weights that may be held as pairs of
+16-bit values (2^-16 relative), sums them in fp32 and is rounded once to its type.
+"""
+import numpy as np
+import pytest
+import torch
+
+import sparse_selection_primitive_b200 as L
+from tests import select_reference as R
+
+pytestmark = pytest.mark.gpu
+HALF = [torch.bfloat16, torch.float16]
+
+
+def caches(seed, B, Sq, Hq, Hkv, N, D, dtype, layout="bhnd"):
+    gen = torch.Generator().manual_seed(seed)
+    q = (torch.randn((B, Sq, Hq, D), generator=gen) * 1.5).to(dtype)
+    if layout == "bhnd":
+        k, v = (torch.randn((B, Hkv, N, D), generator=gen).to(dtype) for _ in range(2))
+    else:  # rows of all heads next to each other
+        k, v = (torch.randn((B, N, Hkv, D), generator=gen).to(dtype).transpose(1, 2)
+                for _ in range(2))
+    score = torch.rand((B, Hkv, N), generator=gen)
+    return q, k, v, score
+
+
+def check_attend(q, k, v, lengths, score, scale=None):
+    """One call against the reference; rows of the caches behind the lengths are NaN, and
+    scores there have to stay."""
+    B, Sq, Hq, D = q.shape
+    N = k.shape[2]
+    n = torch.tensor(lengths, dtype=torch.int32)
+    inside = torch.arange(N)[None, None, :] < n[:, None, None]
+    k, v = (torch.where(inside[..., None], c, torch.full((), float("nan"), dtype=c.dtype))
+            for c in (k, v))
+    # the view keeps its layout
+    kc, vc = (torch.empty_strided(c.shape, o.stride(), dtype=c.dtype, device="cuda").copy_(c)
+              for c, o in ((k, k), (v, v)))
+    sc = score.cuda()
+    args = {} if scale is None else dict(scale=scale)
+    out = L.attend_accumulate(q.cuda(), kc, vc, n.cuda(), sc, **args)
+    scale = D ** -0.5 if scale is None else scale
+    q64, k64, v64 = (c.double().numpy() for c in (q, k, v))
+    o_ref, s_ref = R.attend(q64, np.nan_to_num(k64), np.nan_to_num(v64), lengths, score.numpy(), scale)
+    out, got = out.cpu().double().numpy(), sc.cpu().double().numpy()
+    assert np.array_equal(got[~inside.expand_as(score).numpy()],
+                          score.double().numpy()[~inside.expand_as(score).numpy()])
+    reach = np.abs(q64).max() * np.abs(np.nan_to_num(k64)).max() * D * abs(scale)
+    # the exponent's error is of sums of D terms whose magnitudes average to a tenth of reach
+    rel = (D * reach / 10 + 2 * reach + 64) * 2.0 ** -24
+    grown = s_ref - score.double().numpy()
+    # relative errors hold for normal fp32 numbers only: each of a key's Sq * G weights below
+    # 2^-126 (a reference of 1e-57 among them) may read as 0
+    low = Sq * (Hq // k.shape[1]) * 2.0 ** -126
+    off = np.abs(got - s_ref) - (rel * grown + 2.0 ** -23 * s_ref + low)
+    assert (off <= 0).all(), off.max()
+    unit = R.UNIT[q.dtype]
+    vmax = np.abs(np.nan_to_num(v64)).max()
+    tol = (rel + 2.0 ** -16) * vmax + unit * np.abs(o_ref) * 1.01 + 2.0 ** -24
+    off = np.abs(out - o_ref) - tol
+    assert (off <= 0).all(), off.max()
+    return out, got
+
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("B,Sq,Hq,Hkv,N,D", [
+    (1, 1, 1, 1, 1, 16), (1, 1, 4, 4, 7, 64), (2, 1, 8, 2, 129, 128), (1, 1, 8, 1, 1000, 128),
+    (3, 1, 6, 2, 333, 96), (1, 1, 16, 1, 513, 256), (2, 1, 5, 1, 128, 80), (1, 1, 2, 2, 4097, 64),
+    (1, 1, 40, 2, 700, 128), (1, 1, 12, 4, 255, 48), (2, 1, 64, 1, 400, 64), (1, 1, 1, 1, 383, 192)])
+def test_attend_one_token(cuda_device, dtype, B, Sq, Hq, Hkv, N, D):
+    q, k, v, score = caches(N + D, B, Sq, Hq, Hkv, N, D, dtype)
+    check_attend(q, k, v, [N] * B, score)
+    check_attend(q, k, v, [max(0, N - 3 * b - 1) for b in range(B)], score)
+
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("B,Sq,Hq,Hkv,N,D", [
+    (1, 2, 4, 2, 10, 64), (2, 5, 6, 2, 200, 128), (1, 17, 8, 2, 300, 64), (2, 32, 4, 1, 140, 128),
+    (1, 64, 2, 1, 64, 96), (1, 130, 2, 2, 131, 64), (1, 9, 24, 2, 650, 128), (2, 7, 3, 3, 5, 32)])
+def test_attend_several_tokens(cuda_device, dtype, B, Sq, Hq, Hkv, N, D):
+    q, k, v, score = caches(N + Sq, B, Sq, Hq, Hkv, N, D, dtype)
+    check_attend(q, k, v, [N] * B, score)
+    check_attend(q, k, v, [max(0, N - 60 * (b + 1)) for b in range(B)], score)
+
+
+def test_attend_empty_and_short_sequences(cuda_device):
+    """Lengths of zero and one, shorter than Sq, beyond N and below 0."""
+    q, k, v, score = caches(1, 6, 3, 4, 2, 150, 64, torch.bfloat16)
+    out, got = check_attend(q, k, v, [0, 1, 2, 3, 150, 130], score)
+    assert (out[0] == 0).all() and (out[1, :2] == 0).all()
+    n = torch.tensor([1000, -5, 3, 3, 3, 3], dtype=torch.int32).cuda()
+    s1, s2 = score.cuda(), score.cuda()
+    a = L.attend_accumulate(q.cuda(), k.cuda(), v.cuda(), n, s1)
+    b = L.attend_accumulate(q.cuda(), k.cuda(), v.cuda(), n.clamp(0, 150), s2)
+    assert torch.equal(a, b) and torch.equal(s1, s2)
+
+
+def test_attend_views_and_layouts(cuda_device):
+    q, k, v, score = caches(2, 2, 2, 8, 2, 210, 128, torch.bfloat16, layout="bnhd")
+    check_attend(q, k, v, [210, 77], score)
+    # a cache with room behind, heads sliced out of a wider projection, a score view
+    wide = torch.randn((2, 2, 12, 128)).to(torch.bfloat16).cuda()
+    cache = torch.randn((2, 2, 2, 512, 128)).to(torch.bfloat16).cuda()
+    big = torch.rand((2, 2, 1024), device="cuda")
+    n = torch.tensor([300, 512], dtype=torch.int32, device="cuda")
+    s1, s2 = big[:, :, 100:612], big[:, :, 100:612].contiguous()
+    keep = big.clone()
+    a = L.attend_accumulate(wide[:, :, 2:10], cache[0], cache[1], n, s1)
+    b = L.attend_accumulate(wide[:, :, 2:10].contiguous(), cache[0].clone(), cache[1].clone(), n, s2)
+    assert torch.equal(a, b) and torch.equal(s1, s2)
+    assert torch.equal(big[:, :, :100], keep[:, :, :100]) and torch.equal(big[:, :, 612:], keep[:, :, 612:])
+    # one key/value head broadcast over the heads' dimension
+    c, d = L.attend_accumulate(wide[:, :, :4], cache[0][:, :1].expand(2, 2, 512, 128),
+                               cache[1][:, :1].expand(2, 2, 512, 128), n, s2.clone()), None
+    d = L.attend_accumulate(wide[:, :, :4], cache[0][:, :1].repeat(1, 2, 1, 1),
+                            cache[1][:, :1].repeat(1, 2, 1, 1), n, s2.clone())
+    assert torch.equal(c, d)
+
+
+def test_attend_score_out_and_scale(cuda_device):
+    q, k, v, score = caches(3, 2, 1, 4, 2, 300, 64, torch.float16)
+    check_attend(q, k, v, [300, 9], score, scale=0.3)
+    check_attend(q, k, v, [300, 9], score, scale=0.0)
+    n = torch.tensor([300, 9], dtype=torch.int32).cuda()
+    s = score.cuda()
+    into = torch.full_like(s, 7.0)
+    a = L.attend_accumulate(q.cuda(), k.cuda(), v.cuda(), n, s, score_out=into)
+    assert torch.equal(s, score.cuda()) and (into[1, :, 9:] == 7.0).all()
+    out = torch.empty_like(a)
+    b = L.attend_accumulate(q.cuda(), k.cuda(), v.cuda(), n, s, out=out)
+    assert b is out and torch.equal(a, b) and torch.equal(s[0], into[0])
+
+
+def test_attend_sharp_and_flat_rows(cuda_device):
+    """Logits hundreds apart (weights that underflow), equal keys, and one hot key in the last place."""
+    q, k, v, score = caches(4, 1, 1, 4, 1, 600, 64, torch.bfloat16)
+    score.zero_()
+    out, got = check_attend(q * 8, k * 4, v, [600], score)
+    same = k[:, :, :1].expand_as(k).contiguous()
+    out, got = check_attend(q, same, v, [600], score)
+    hot = k * 0.01
+    hot[0, 0, 599] = (q[0, 0, 0] * 40).to(hot.dtype)
+    check_attend(q, hot, v, [600], score)
+
+
+def test_attend_refusals(cuda_device):
+    q, k, v, score = (c.cuda() for c in caches(5, 2, 1, 4, 2, 40, 64, torch.bfloat16))
+    n = torch.tensor([40, 40], dtype=torch.int32).cuda()
+    ok = lambda **o: L.attend_accumulate(**{**dict(q=q, k=k, v=v, lengths=n, score=score), **o})  # noqa: E731
+    ok()
+    for bad in (dict(q=q.float()), dict(q=q.half()), dict(k=k.float()), dict(lengths=n.long()),
+                dict(score=score.double()), dict(q=q.cpu())):
+        with pytest.raises(TypeError):
+            ok(**bad)
+    for bad in (dict(q=q[:, :, :3]), dict(v=v[:, :, :39]), dict(score=score[:, :, :39]),
+                dict(lengths=n[:1]), dict(k=k[..., :32]), dict(q=q[:1]),
+                dict(score_out=score[:, :, :1].expand_as(score)), dict(out=q),
+                dict(score=score[:1].expand(2, 2, 40)), dict(out=torch.empty_like(q)[:1])):
+        with pytest.raises(ValueError):
+            ok(**bad)
+    with pytest.raises(ValueError):   # half an overlap
+        big = torch.zeros((2, 2, 50), device="cuda")
+        ok(score=big[:, :, :40], score_out=big[:, :, 5:45])
+    for D in (8, 24, 272):            # no multiple of 16, or too wide
+        w = torch.zeros((1, 1, 4, D), dtype=torch.bfloat16, device="cuda")
+        with pytest.raises(L.LapSumError):
+            L.attend_accumulate(w[:, :, :1], w, w, n[:1], torch.zeros((1, 1, 4), device="cuda"))
+    off = torch.zeros(2 * 2 * 40 * 64 + 4, dtype=torch.bfloat16, device="cuda")[4:].view(2, 2, 40, 64)
+    with pytest.raises(L.LapSumError):  # rows that do not start on 16 bytes
+        ok(k=off)
+
+
+def check_evict(k, v, score, lengths, budget, first=0, last=0, out=None):
+    B, H, N, D = k.shape
+    n = torch.tensor(lengths, dtype=torch.int32).cuda()
+    e = L.evict(k, v, score, n, budget, first=first, last=last, out=out)
+    pos = e.positions.cpu().numpy()
+    s = score.cpu().numpy()
+    for b in range(B):
+        m = min(max(int(lengths[b]), 0), N)
+        assert int(e.lengths[b]) == min(m, budget)
+        for h in range(H):
+            ref = R.evict_positions(s[b, h, :m], m, budget, first, last)
+            assert np.array_equal(pos[b, h, :ref.size], ref), (b, h)
+            assert (pos[b, h, ref.size:] == -1).all()
+            at = torch.from_numpy(ref).to(k.device)
+            bits = lambda t: t.contiguous().view(torch.int32 if t.element_size() == 4 else torch.int16)  # noqa: E731
+            if ref.size:
+                assert torch.equal(bits(e.k[b, h, :ref.size]), bits(k[b, h, at]))
+                assert torch.equal(bits(e.v[b, h, :ref.size]), bits(v[b, h, at]))
+                assert torch.equal(bits(e.score[b, h, :ref.size]), bits(score[b, h, at]))
+            for x in (e.k, e.v, e.score):
+                assert (x[b, h, ref.size:budget] == 0).all()
+    return e
+
+
+def evict_inputs(seed, B, H, N, D, dtype, kind="normal"):
+    gen = torch.Generator().manual_seed(seed)
+    k, v = (torch.randn((B, H, N, D), generator=gen).to(dtype).cuda() for _ in range(2))
+    s = torch.randn((B, H, N), generator=gen)
+    if kind == "ties":
+        s = (s * 4).round() / 4
+    if kind == "small":
+        s = (s * 3 - 12).exp()
+    if kind == "same":
+        s = torch.ones_like(s)
+    return k, v, s.cuda()
+
+
+@pytest.mark.parametrize("kind", ["normal", "ties", "small", "same"])
+@pytest.mark.parametrize("B,H,N,D,budget,first,last", [
+    (1, 1, 1, 1, 1, 0, 0), (1, 2, 10, 8, 3, 1, 1), (2, 2, 513, 64, 100, 4, 16), (1, 3, 700, 96, 512, 0, 0),
+    (2, 1, 5000, 16, 1024, 4, 128), (1, 1, 20000, 4, 1, 0, 0), (1, 1, 20000, 4, 19999, 0, 1),
+    (1, 2, 1025, 128, 1025, 3, 7), (1, 1, 9000, 24, 40, 8, 32)])
+def test_evict(cuda_device, kind, B, H, N, D, budget, first, last):
+    for dtype in (torch.bfloat16, torch.float32):
+        k, v, s = evict_inputs(N + D, B, H, N, D, dtype, kind)
+        check_evict(k, v, s, [max(1, N - 37 * b) for b in range(B)], budget, first, last)
+
+
+def test_evict_short_rows(cuda_device):
+    """Lengths of zero, one, the budget and one more; lengths beyond N and below 0."""
+    k, v, s = evict_inputs(1, 7, 2, 64, 32, torch.float16)
+    check_evict(k, v, s, [0, 1, 10, 11, 64, 99, -3], 10, 2, 3)
+    check_evict(k, v, s, [0, 1, 10, 11, 64, 99, -3], 100, 2, 3)  # a budget above N
+
+
+def test_evict_odd_scores(cuda_device):
+    """NaN below every number, infinities, -0 equal to +0, denormals."""
+    k, v, s = evict_inputs(2, 1, 4, 300, 8, torch.bfloat16)
+    s[0, 0, ::3] = float("nan")
+    s[0, 1, ::2] = float("inf")
+    s[0, 1, 1::4] = -float("inf")
+    s[0, 2] = torch.where(torch.arange(300, device="cuda") % 2 == 0, 0.0, -0.0)
+    s[0, 3] = torch.arange(300, device="cuda") * 1e-44
+    for budget in (1, 50, 199, 260, 299):
+        check_evict(k, v, s, [300], budget, 0, 0)
+    s[:] = float("nan")
+    check_evict(k, v, s, [300], 7, 1, 1)
+
+
+def test_evict_views_and_out(cuda_device):
+    B, H, N, D, budget = 2, 3, 400, 40, 64
+    base = torch.randn((2, B, N, H, D)).to(torch.bfloat16).cuda()
+    k, v = base[0].transpose(1, 2), base[1].transpose(1, 2)
+    score = torch.randn((B, N, H), device="cuda").transpose(1, 2)
+    with pytest.raises(ValueError):      # scores of a head must be consecutive
+        L.evict(k, v, score, torch.tensor([N] * B, dtype=torch.int32).cuda(), budget)
+    score = torch.randn((B, H, N + 9), device="cuda")[:, :, 5:N + 5]
+    check_evict(k, v, score, [N, 200], budget, 2, 8)
+    room = torch.full((2, B, budget + 50, H, D), 3.0, dtype=torch.bfloat16, device="cuda")
+    so = torch.full((B, H, budget + 50), 3.0, device="cuda")
+    out = (room[0].transpose(1, 2), room[1].transpose(1, 2), so)
+    e = check_evict(k, v, score, [N, 20], budget, 2, 8, out=out)
+    assert e.k is out[0] and (e.k[:, :, budget:] == 3).all() and (e.v[:, :, budget:] == 3).all()
+    assert (so[:, :, budget:] == 3).all()
+    odd = torch.randn((B, H, N, 41), device="cuda")[..., 1:]      # rows off 8 and 16 bytes
+    check_evict(odd, odd.clone(), score, [N, 20], budget)
+
+
+def test_evict_refusals(cuda_device):
+    k, v, s = evict_inputs(3, 1, 2, 40, 16, torch.bfloat16)
+    n = torch.tensor([40], dtype=torch.int32).cuda()
+    for bad in (dict(budget=0), dict(budget=5, first=3, last=3), dict(budget=5, first=-1)):
+        with pytest.raises(ValueError):
+            L.evict(k, v, s, n, **bad)
+    with pytest.raises(ValueError):
+        L.evict(k, v, s, n, 8, out=(k, v, s))
+    with pytest.raises(ValueError):
+        L.evict(k, v[:, :, :39], s, n, 8)
+    with pytest.raises(TypeError):
+        L.evict(k, v.float(), s, n, 8)
+    with pytest.raises(ValueError):      # room for fewer rows than the budget
+        L.evict(k, v, s, n, 8, out=(torch.empty_like(k)[:, :, :7], torch.empty_like(v), torch.empty_like(s)))
+
+
+def test_decode_with_eviction(cuda_device):
+    """A run of decoding steps over a cache: append a key, attend and accumulate, evict when
+    the cache is full, go on over the compacted cache -- against the same run in float64."""
+    B, H, G, D, C, budget, steps = 2, 2, 3, 64, 96, 40, 90
+    gen = torch.Generator().manual_seed(9)
+    kc, vc = (torch.full((B, H, C, D), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    spare = (torch.full_like(kc, float("nan")), torch.full_like(vc, float("nan")),
+             torch.zeros((B, H, C), device="cuda"))
+    sc = torch.zeros((B, H, C), device="cuda")
+    n = 0
+    for step in range(steps):
+        q = (torch.randn((B, 1, H * G, D), generator=gen) * 1.5).to(torch.bfloat16).cuda()
+        kc[:, :, n], vc[:, :, n] = (torch.randn((B, H, D), generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+        sc[:, :, n] = 0
+        n += 1
+        lengths = torch.full((B,), n, dtype=torch.int32, device="cuda")
+        before = sc.clone()
+        out = L.attend_accumulate(q, kc, vc, lengths, sc)
+        o_ref, s_ref = R.attend(q.double().cpu().numpy(), kc.double().nan_to_num().cpu().numpy(),
+                                vc.double().nan_to_num().cpu().numpy(), [n] * B,
+                                before.cpu().numpy(), D ** -0.5)
+        # logits of 64 products: errors of the weights below 2^-12; out rounded to bf16
+        assert np.abs(out.double().cpu().numpy() - o_ref).max() <= 4.5 * (2.0 ** -8 + 2.0 ** -12)
+        assert np.abs(sc.double().cpu().numpy() - s_ref).max() <= 2.0 ** -12 * G
+        if n == C:
+            e = check_evict(kc, vc, sc, [n] * B, budget, 2, 8, out=spare)
+            spare, (kc, vc, sc) = (kc, vc, sc), (e.k, e.v, e.score)
+            n = budget
+    assert n < C
+
+
+def test_cache_other_streams_and_capture(cuda_device):
+    q, k, v, score = (c.cuda() for c in caches(6, 2, 2, 8, 2, 500, 64, torch.bfloat16))
+    n = torch.tensor([500, 123], dtype=torch.int32).cuda()
+
+    def step(s):
+        o = L.attend_accumulate(q, k, v, n, s)
+        return (o, s) + tuple(L.evict(k, v, s, n, 64, first=2, last=10))
+
+    want = step(score.clone())
+    torch.cuda.synchronize()
+    got = []
+    for stream in (torch.cuda.Stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(stream):
+            for _ in range(4):
+                r = step(score.clone())
+            got.append(r)
+    torch.cuda.synchronize()
+    for r in got:
+        assert all(torch.equal(a, b) for a, b in zip(r, want))
+    # two graphs over the same inputs, replayed in turn with other contents
+    graphs = []
+    for _ in range(2):
+        s = score.clone()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            r = step(s)
+        graphs.append((g, s, r))
+    for seed in (1, 2):
+        q.copy_(torch.randn(q.shape, generator=torch.Generator().manual_seed(seed)))
+        n.copy_(torch.tensor([400 + seed, 10 * seed], dtype=torch.int32))
+        want = step(score.clone())
+        for g, s, r in graphs:
+            s.copy_(score)
+            g.replay()
+            assert all(torch.equal(a, b) for a, b in zip(r, want))
+
+
+def test_attend_is_repeatable(cuda_device):
+    """No result depends on the order in which blocks run."""
+    q, k, v, score = (c.cuda() for c in caches(7, 2, 3, 8, 2, 3000, 128, torch.bfloat16))
+    n = torch.tensor([3000, 1777], dtype=torch.int32).cuda()
+    first = None
+    for _ in range(5):
+        s = score.clone()
+        o = L.attend_accumulate(q, k, v, n, s)
+        if first is None:
+            first = (o, s)
+        assert torch.equal(o, first[0]) and torch.equal(s, first[1])
