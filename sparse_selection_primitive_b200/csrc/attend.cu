@@ -1,10 +1,20 @@
 // Attention over a cache that also accumulates, per key, the weight that the
 // queries gave it.  Entry point: lapsum_attend_accumulate (include/lapsum.h).
 //
-// For each sequence b, key/value head h and query row r (a token and one of the
+// For each sequence b, key/value head h and query row r = i G + g (token i, and g of the
 // G = Hq / Hkv query heads that share h):
-//     x_j = scale q_r . k_j  over the keys the query sees,  p = softmax(x),
+//     x_j = scale q_r . k_j  over the keys the row sees,  p = softmax(x),
 //     out_r = sum_j p_j v_j,   score[b, h, j] += sum_r p_{r, j}.
+//
+// Keys take the M side of the matrix instruction: S^T = K Q^T is 128 keys x RT rows, so
+// that a few query rows (one token and its G heads) fill a whole instruction, each
+// thread holds one key's logits for all rows, and the column sums that the scores need are
+// sums inside a thread.  A block takes a run of key tiles small enough that all their
+// logits stay in tensor memory; it therefore knows the run's maximum before it forms any
+// weight, and O^T = V^T P (D x RT, V read as it lies) needs no rescaling.  Weights go to
+// the second product as pairs of 16-bit values, p = hi + lo, so that they keep 16 bits
+// and more of p.  Runs are joined by a second kernel, which also turns logits into scores.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -12,19 +22,37 @@
 #include "elements.cuh"
 #include "lapsum_common.cuh"
 #include "lapsum_kernels.h"
+#include "tensor_core.cuh"
 
 namespace lapsum {
 namespace {
 
-constexpr int kAttThreads = 128;
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kTile = 128;          // keys per tile: the M of S^T
+constexpr int kSplitThreads = 192;  // warp 0 loads, warp 1 multiplies, warps 2-5 do the softmax
+constexpr int kMaxStages = 6;
+constexpr int kMaxTiles = 32;
+constexpr int kJoinThreads = 256;
 
 struct AttendArgs {
-    int64_t qb, qh, qr, kb, kh, kr, vb, vh, vr, sib, sih, sob, soh;
-    int64_t B, Sq, Hq, Hkv, N;
-    int D, G;
-    float scale;
+    int64_t qb, qh, qr;  // element strides of q: batch, head, token
+    int64_t sib, sih, sob, soh;
+    int64_t N, R;        // rows per key/value head: Sq * G
+    int B, Sq, Hkv, D, G;
+    int kh, kb, vh, vb;  // 1 where the caches' head and batch coordinates count, else 0
+    float scale_log2;    // scale * log2(e): logits and weights are kept in powers of two
     const int32_t* lengths;
+};
+
+// How the work is cut; a function of the sizes alone.
+struct AttendPlan {
+    int rt;         // rows per tile
+    int row_tiles;
+    int splits;     // runs of key tiles per row tile
+    int tiles;      // most key tiles per run
+    int stages, cols, smem;
+    int64_t RP;     // rows of logits per key, padded
+    size_t off_part, off_logits, bytes;
 };
 
 __device__ __forceinline__ int64_t cache_length(const AttendArgs& a, int64_t b) {
@@ -32,82 +60,558 @@ __device__ __forceinline__ int64_t cache_length(const AttendArgs& a, int64_t b) 
     return n < 0 ? 0 : n > a.N ? a.N : n;
 }
 
-// One block per query row: logits into the workspace, then the weighted sum.
-template <class T>
-__global__ void __launch_bounds__(kAttThreads)
-    attend_rows_kernel(AttendArgs a, const T* q, const T* k, const T* v, T* out, float* logits,
-                       float* lse) {
-    pdl_wait();
-    __shared__ float sq[256], red[kAttThreads / 32];
-    const int64_t row = blockIdx.x;  // ((b * Sq) + i) * Hq + head
-    const int64_t head = row % a.Hq, i = row / a.Hq % a.Sq, b = row / a.Hq / a.Sq, h = head / a.G;
-    const int64_t n = cache_length(a, b);
-    const int64_t see = n - a.Sq + i + 1 < 0 ? 0 : n - a.Sq + i + 1;
-    for (int d = threadIdx.x; d < a.D; d += kAttThreads)
-        sq[d] = widen(q[b * a.qb + i * a.qr + head * a.qh + d]) * a.scale;
-    __syncthreads();
-    float* x = logits + row * a.N;
-    const T* kp = k + b * a.kb + h * a.kh;
-    const T* vp = v + b * a.vb + h * a.vh;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float m = -INFINITY;
-    for (int64_t j = threadIdx.x; j < see; j += kAttThreads) {
-        float s = 0.f;
-        for (int d = 0; d < a.D; ++d) s = fmaf(sq[d], widen(kp[j * a.kr + d]), s);
-        x[j] = s;
-        m = fmaxf(m, s);
-    }
+// v[i] of all 32 lanes joined, N values: afterwards lane l holds the results of
+// N / 32 (or 1) values from index joined_at<N>(l) on.  Each step halves the values a lane
+// still holds, so the whole costs about N exchanges instead of 5 N.
+template <int N>
+__device__ __forceinline__ int joined_at(int lane) {
+    int at = 0, half = N / 2;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, d));
-    if (lane == 0) red[warp] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    __syncthreads();
-    float l = 0.f;
-    for (int64_t j = threadIdx.x; j < see; j += kAttThreads) l += expf(x[j] - m);
+    for (int d = 16; d; d >>= 1)
+        if (half >= 1) {
+            at += (lane & d) ? half : 0;
+            half >>= 1;
+        }
+    return at;
+}
+template <int N, class F>
+__device__ __forceinline__ void join_lanes(float (&v)[N], int lane, F f) {
+    int n = N;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(kAll, l, d);
-    if (lane == 0) red[warp] = l;
-    __syncthreads();
-    l = red[0] + red[1] + red[2] + red[3];
-    if (threadIdx.x == 0) lse[row] = see > 0 ? m + logf(l) : INFINITY;
-    for (int d = threadIdx.x; d < a.D; d += kAttThreads) {
-        float o = 0.f;
-        for (int64_t j = 0; j < see; ++j) o = fmaf(expf(x[j] - m), widen(vp[j * a.vr + d]), o);
-        out[row * a.D + d] = narrow<T>(see > 0 ? o / l : 0.f);
+    for (int d = 16; d; d >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool up = lane & d;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i)
+                if (i < n) {
+                    const float give = up ? v[i] : v[i + n], keep = up ? v[i + n] : v[i];
+                    v[i] = f(keep, __shfl_xor_sync(kAll, give, d));
+                }
+        } else {
+            v[0] = f(v[0], __shfl_xor_sync(kAll, v[0], d));
+        }
     }
 }
 
-__global__ void __launch_bounds__(kAttThreads)
-    attend_score_kernel(AttendArgs a, const float* logits, const float* lse, const float* score_in,
-                        float* score_out) {
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+template <class T>
+struct Pair;  // two 16-bit values in a word
+template <>
+struct Pair<__nv_bfloat16> {
+    static constexpr bool bf16 = true;
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&p);
+    }
+};
+template <>
+struct Pair<__half> {
+    static constexpr bool bf16 = false;
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const __half2 p = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&p);
+    }
+};
+
+// One run of key tiles for one tile of rows.  Writes the run's row maxima and sums
+// (stats), its unnormalised outputs (part) and the logits, all in fp32.
+template <class T, int RT>
+__global__ void __launch_bounds__(kSplitThreads)
+    attend_split_kernel(AttendArgs a, AttendPlan p, const T* q,
+                        const __grid_constant__ CUtensorMap k_map,
+                        const __grid_constant__ CUtensorMap v_map, float2* stats, float* part,
+                        float* logits) {
+    extern __shared__ char smem_raw[];
+    __shared__ uint64_t bars[2 * kMaxStages + kMaxTiles + 2];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_failed;
+    __shared__ float red[4][RT];
+    __shared__ alignas(16) float s_max[RT];
+    __shared__ alignas(16) int s_lim[RT];  // keys that each row sees, from the run's first
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rt = blockIdx.x % p.row_tiles;
+    const int64_t rest = blockIdx.x / p.row_tiles;
+    const int split = (int)(rest % p.splits);
+    const int64_t bh = rest / p.splits;
+    const int b = (int)(bh / a.Hkv), h = (int)(bh % a.Hkv);
+    const int64_t row0 = (int64_t)rt * RT;
+    const int rows = (int)(a.R - row0 < RT ? a.R - row0 : RT);
+    float2* my_stats = stats + (bh * p.splits + split) * a.R + row0;
+
     pdl_wait();
-    const int64_t bh = blockIdx.y + (int64_t)gridDim.y * blockIdx.z, b = bh / a.Hkv, h = bh % a.Hkv;
-    if (b >= a.B) return;
     const int64_t n = cache_length(a, b);
-    for (int64_t j = (int64_t)blockIdx.x * kAttThreads + threadIdx.x; j < n;
-         j += (int64_t)gridDim.x * kAttThreads) {
-        float s = 0.f;
-        for (int64_t i = 0; i < a.Sq; ++i) {
-            if (j >= n - a.Sq + i + 1) continue;
-            for (int g = 0; g < a.G; ++g) {
-                const int64_t row = (b * a.Sq + i) * a.Hq + h * a.G + g;
-                s += expf(logits[row * a.N + j] - lse[row]);
+    // keys that the tile's last row sees, and this run's tiles among them
+    int64_t seen = n - a.Sq + 1 + (row0 + rows - 1) / a.G;
+    seen = seen < 0 ? 0 : seen;
+    const int64_t all_tiles = (seen + kTile - 1) / kTile;
+    const int64_t per = (all_tiles + p.splits - 1) / p.splits;
+    const int64_t first = split * per;
+    const int tiles = (int)(all_tiles - first < per ? all_tiles - first : per);
+    if (tiles <= 0) {
+        if (threadIdx.x < rows) my_stats[threadIdx.x] = make_float2(-INFINITY, 0.f);
+        return;
+    }
+
+    const int subs = (a.D + 63) / 64;                   // 128-byte column blocks of a row
+    const uint32_t sub_bytes = kTile * 128, stage_bytes = subs * sub_bytes;
+    const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t q_at = ring + p.stages * stage_bytes;
+    const uint32_t p_at = q_at + subs * RT * 128;       // hi, then lo
+    const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages,
+                   s_done = empty + 8 * kMaxStages, p_full = s_done + 8 * kMaxTiles,
+                   p_empty = p_full + 8;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < tiles; ++i) mbar_init(s_done + 8 * i, 1);
+        mbar_init(p_full, 128);
+        mbar_init(p_empty, 1);
+        fence_barrier_init();
+        s_failed = 0;
+    }
+    if (threadIdx.x < RT) {
+        int64_t lim = n - a.Sq + 1 + (row0 + threadIdx.x) / a.G - first * kTile;
+        lim = lim < 0 ? 0 : lim;
+        s_lim[threadIdx.x] = (int)(threadIdx.x < rows && lim < tiles * kTile ? lim : tiles * kTile);
+    }
+    if (warp == 1) tmem_alloc(smem_addr(&s_tmem), p.cols);
+    // the row tile, zero beyond the rows and beyond D, in the layout TMA gives the keys
+    for (int i = threadIdx.x; i < RT * subs * 8; i += kSplitThreads) {
+        const int r = i / (subs * 8), c = i % (subs * 8);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < rows && c * 8 < a.D) {
+            const int64_t row = row0 + r, tok = row / a.G, g = row - tok * a.G;
+            x = *reinterpret_cast<const uint4*>(q + b * a.qb + tok * a.qr +
+                                                ((int64_t)h * a.G + g) * a.qh + c * 8);
+        }
+        const uint32_t at = q_at + (c >> 3) * (RT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y),
+                     "r"(x.z), "r"(x.w)
+                     : "memory");
+    }
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem, o_col = tmem + tiles * RT;
+    const int items = 2 * tiles;  // the run's key tiles, then its value tiles
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int issued = 0;
+            for (; issued < items && ok; ++issued) {
+                const int s = issued % p.stages, turn = issued / p.stages;
+                if (turn > 0) ok = mbar_wait(empty + 8 * s, (turn - 1) & 1);
+                if (!ok) break;
+                mbar_expect(full + 8 * s, stage_bytes);
+                const bool key = issued < tiles;
+                const int y = (int)((first + (key ? issued : issued - tiles)) * kTile);
+                for (int c = 0; c < subs; ++c)
+                    tma_load_4d(ring + s * stage_bytes + c * sub_bytes, key ? &k_map : &v_map,
+                                full + 8 * s, c * 64, y, h * (key ? a.kh : a.vh),
+                                b * (key ? a.kb : a.vb));
+            }
+            if (!ok)  // gave up: let the copies in flight land before the block ends
+                for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+                    mbar_wait(full + 8 * (i % p.stages), (i / p.stages) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t shape_s = mma_shape(Pair<T>::bf16, false, false, kTile, RT);
+            const uint32_t shape_o = mma_shape(Pair<T>::bf16, true, true, 128, RT);
+            for (int t = 0; t < tiles && ok; ++t) {
+                const int s = t % p.stages;
+                ok = mbar_wait(full + 8 * s, (t / p.stages) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                for (int kk = 0; kk * 16 < a.D; ++kk) {
+                    const uint32_t sub = kk >> 2, in = (kk & 3) * 32;
+                    mma_f16(tmem + t * RT,
+                            operand(ring + s * stage_bytes + sub * sub_bytes + in, 16, 1024, kSwizzle128),
+                            operand(q_at + sub * (RT * 128) + in, 16, 1024, kSwizzle128), shape_s,
+                            kk > 0);
+                }
+                mma_commit(empty + 8 * s);
+                mma_commit(s_done + 8 * t);
+            }
+            for (int t = 0; t < tiles && ok; ++t) {
+                const int item = tiles + t, s = item % p.stages;
+                ok = mbar_wait(full + 8 * s, (item / p.stages) & 1) && mbar_wait(p_full, t & 1);
+                if (!ok) break;
+                tc_fence_after();
+                for (int m = 0; m * 128 < a.D; ++m)
+                    for (int kk = 0; kk < kTile / 16; ++kk) {
+                        const uint64_t v = operand(ring + s * stage_bytes + m * 2 * sub_bytes + kk * 2048,
+                                                   sub_bytes, 1024, kSwizzle128);
+                        for (int half = 0; half < 2; ++half)
+                            mma_f16(o_col + m * RT, v,
+                                    operand(p_at + half * (RT * 256) + kk * 256, 128, 2048, kNoSwizzle),
+                                    shape_o, t + kk + half > 0);
+                    }
+                mma_commit(empty + 8 * s);
+                mma_commit(p_empty);
             }
         }
-        const float old = score_in != nullptr ? score_in[b * a.sib + h * a.sih + j] : 0.f;
-        score_out[b * a.sob + h * a.soh + j] = old + s;
+    } else {
+        const int quarter = warp & 3;                  // the lanes of tensor memory it may read
+        const int key = quarter * 32 + lane;           // of a tile
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const int tid = threadIdx.x - 64;
+        float top[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) top[r] = -INFINITY;
+        // phase 1: logits, their maxima
+        for (int t = 0; t < tiles && ok; ++t) {
+            ok = mbar_wait(s_done + 8 * t, 0);
+            if (!__all_sync(kAll, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            float x[RT];
+            tmem_ld<RT>(lanes + t * RT, x);
+            const int64_t j = (first + t) * kTile + key;
+            const bool whole = (t + 1) * kTile <= s_lim[0];  // the first row sees the fewest
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                x[r] *= a.scale_log2;
+                if (!whole && t * kTile + key >= s_lim[r]) x[r] = -INFINITY;
+                top[r] = fmaxf(top[r], x[r]);
+            }
+            if (j < n) {
+                float* to = logits + (bh * a.N + j) * p.RP + row0;
+#pragma unroll
+                for (int r = 0; r < RT; r += 4)
+                    if (row0 + r < p.RP)
+                        *reinterpret_cast<float4*>(to + r) =
+                            make_float4(x[r], x[r + 1], x[r + 2], x[r + 3]);
+            }
+        }
+        join_lanes<RT>(top, lane, [](float u, float w) { return fmaxf(u, w); });
+        constexpr int kOwn = RT > 32 ? RT / 32 : 1;
+        const int at = joined_at<RT>(lane);
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) red[quarter][at + i] = top[i];
+        softmax_sync();
+        if (tid < RT) {
+            const float m = fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid]));
+            s_max[tid] = m == -INFINITY ? 0.f : m;
+        }
+        softmax_sync();
+        // phase 2: weights relative to the run's maximum
+        float sum[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) sum[r] = 0.f;
+        for (int t = 0; t < tiles && ok; ++t) {
+            float x[RT];
+            tmem_ld<RT>(lanes + t * RT, x);
+            const int64_t j0 = (first + t) * kTile, j = j0 + key;
+            const bool whole = (t + 1) * kTile <= s_lim[0];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                x[r] = ex2_ftz(__fmul_rn(x[r], a.scale_log2) - s_max[r]);
+                if (!whole && t * kTile + key >= s_lim[r]) x[r] = 0.f;
+                sum[r] += x[r];
+            }
+            if (t > 0) ok = mbar_wait(p_empty, (t - 1) & 1);
+            if (j0 + kTile > n) {
+                // value rows behind the cache's end may hold anything: 0 x NaN is NaN
+                const int item = tiles + t, s = item % p.stages;
+                ok = ok && mbar_wait(full + 8 * s, (item / p.stages) & 1);
+                if (j >= n)
+                    for (int c = 0; c < subs * 8; ++c)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         ring + s * stage_bytes + (c >> 3) * sub_bytes + key * 128 +
+                                         (c & 7) * 16),
+                                     "r"(0)
+                                     : "memory");
+            }
+            if (!__all_sync(kAll, ok)) {
+                ok = false;
+                break;
+            }
+#pragma unroll
+            for (int r = 0; r < RT; r += 8) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float u = x[r + 2 * i], w = x[r + 2 * i + 1];
+                    hi[i] = Pair<T>::pack(u, w);
+                    const T* parts = reinterpret_cast<const T*>(&hi[i]);
+                    lo[i] = Pair<T>::pack(u - widen(parts[0]), w - widen(parts[1]));
+                }
+                const uint32_t to = p_at + (r >> 3) * 2048 + key * 16;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]),
+                             "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
+                             : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + RT * 256),
+                             "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
+                             : "memory");
+            }
+            fence_async_smem();
+            tc_fence_before();
+            mbar_arrive(p_full);
+        }
+        join_lanes<RT>(sum, lane, [](float u, float w) { return u + w; });
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) red[quarter][at + i] = sum[i];
+        if (ok) ok = mbar_wait(p_empty, (tiles - 1) & 1);
+        if (!ok) s_failed = 1;
+        softmax_sync();
+        tc_fence_after();
+        if (tid < rows) {
+            const float l = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
+            // a wait that ran out leaves NaN, which the answer then shows
+            my_stats[tid] = s_failed ? make_float2(NAN, NAN)
+                            : l > 0.f || isnan(l) ? make_float2(s_max[tid], l)
+                                                  : make_float2(-INFINITY, 0.f);
+        }
+        if (!s_failed)
+            for (int m = 0; m * 128 < a.D; ++m) {
+                float o[RT];
+                tmem_ld<RT>(lanes + tiles * RT + m * RT, o);
+                const int d = m * 128 + key;
+                if (d < a.D) {
+                    float* to = part + ((bh * p.splits + split) * a.R + row0) * a.D + d;
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+                        if (r < rows) to[(int64_t)r * a.D] = o[r];
+                }
+            }
+        tc_fence_before();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free(tmem, p.cols);
     }
 }
+
+// log2 of the sum of 2^x over all of a row's runs; +inf for a row that saw nothing.
+__device__ __forceinline__ float row_lse(const float2* stats, int splits, int64_t R) {
+    float m = -INFINITY;
+    bool bad = false;
+    for (int s = 0; s < splits; ++s) {
+        const float2 x = stats[s * R];
+        bad |= isnan(x.x) || isnan(x.y);
+        m = fmaxf(m, x.x);
+    }
+    if (bad) return NAN;
+    float l = 0.f;
+    for (int s = 0; s < splits; ++s) {
+        const float2 x = stats[s * R];
+        if (x.y > 0.f) l += x.y * ex2_ftz(x.x - m);
+    }
+    return l > 0.f ? m + log2f(l) : INFINITY;
+}
+
+// Joins the runs.  The first blocks turn logits into scores, one thread a key; the
+// others join the outputs, one warp a row.
+template <class T>
+__global__ void __launch_bounds__(kJoinThreads)
+    attend_join_kernel(AttendArgs a, AttendPlan p, int64_t score_blocks, int key_blocks,
+                       const float2* stats, const float* part, const float* logits,
+                       const float* score_in, float* score_out, T* out) {
+    pdl_wait();
+    constexpr int kRows = 1024;
+    __shared__ alignas(16) float lse[kRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.x < score_blocks) {
+        const int64_t bh = blockIdx.x / key_blocks, b = bh / a.Hkv, h = bh - b * a.Hkv;
+        const int64_t n = cache_length(a, b);
+        const int64_t j0 = (int64_t)(blockIdx.x % key_blocks) * kJoinThreads, j = j0 + threadIdx.x;
+        if (j0 >= n) return;
+        // rows from this one on see key j
+        const int64_t past = j - (n - a.Sq);
+        const int64_t from = past > 0 ? past * a.G : 0;
+        float s = 0.f;
+        for (int64_t base = 0; base < p.RP; base += kRows) {
+            const int cnt = (int)(p.RP - base < kRows ? p.RP - base : kRows);
+            __syncthreads();
+            for (int r = threadIdx.x; r < cnt; r += kJoinThreads)
+                lse[r] = base + r < a.R
+                             ? row_lse(stats + bh * p.splits * a.R + base + r, p.splits, a.R)
+                             : INFINITY;
+            __syncthreads();
+            if (j < n) {
+                const float* x = logits + (bh * a.N + j) * p.RP + base;
+                int r = (int)(from > base ? (from - base < cnt ? from - base : cnt) : 0) & ~3;
+                for (; r < cnt; r += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(x + r);
+                    const float4 w = *reinterpret_cast<const float4*>(lse + r);
+                    s += ex2_ftz(v.x - w.x) + ex2_ftz(v.y - w.y);
+                    s += ex2_ftz(v.z - w.z) + ex2_ftz(v.w - w.w);
+                }
+            }
+        }
+        if (j < n) {
+            const float old = score_in != nullptr ? score_in[b * a.sib + h * a.sih + j] : 0.f;
+            score_out[b * a.sob + h * a.soh + j] = old + s;
+        }
+        return;
+    }
+    const int64_t row = (blockIdx.x - score_blocks) * (kJoinThreads / 32) + warp;
+    if (row >= (int64_t)a.B * a.Hkv * a.R) return;
+    const int64_t bh = row / a.R, r = row - bh * a.R, b = bh / a.Hkv, h = bh - b * a.Hkv;
+    const int64_t tok = r / a.G, g = r - tok * a.G;
+    const float2* st = stats + bh * p.splits * a.R + r;
+    const float top = row_lse(st, p.splits, a.R);  // the same on all lanes
+    T* to = out + ((b * a.Sq + tok) * a.Hkv * a.G + h * a.G + g) * a.D;
+    for (int d = lane * 4; d < a.D; d += 128) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (isnan(top)) {
+            acc = make_float4(NAN, NAN, NAN, NAN);
+        } else {
+            for (int s = 0; s < p.splits; ++s) {
+                const float2 x = st[s * a.R];
+                if (!(x.y > 0.f)) continue;
+                const float w = ex2_ftz(x.x - top);
+                const float4 o = *reinterpret_cast<const float4*>(
+                    part + ((bh * p.splits + s) * a.R + r) * a.D + d);
+                acc.x = fmaf(w, o.x, acc.x);
+                acc.y = fmaf(w, o.y, acc.y);
+                acc.z = fmaf(w, o.z, acc.z);
+                acc.w = fmaf(w, o.w, acc.w);
+            }
+        }
+        Pack<T, 4> o;
+        o.v[0] = narrow<T>(acc.x);
+        o.v[1] = narrow<T>(acc.y);
+        o.v[2] = narrow<T>(acc.z);
+        o.v[3] = narrow<T>(acc.w);
+        *reinterpret_cast<Pack<T, 4>*>(to + d) = o;
+    }
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 bool attend_sizes_ok(int64_t B, int64_t Sq, int64_t Hq, int64_t Hkv, int64_t N, int64_t D) {
     const int64_t big = int64_t(1) << 31;
     return B >= 1 && Sq >= 1 && Hq >= 1 && Hkv >= 1 && N >= 1 && B < 65536 && Sq < 65536 &&
-           Hq < 65536 && N < big && Hq % Hkv == 0 && D >= 16 && D <= 256 && D % 16 == 0 &&
-           B * Sq < big / Hq;
+           Hq < 65536 && Hkv <= Hq && N < big - kTile && Hq % Hkv == 0 && D >= 16 && D <= 256 &&
+           D % 16 == 0 && B * Sq < big / Hq && B * Hkv * ((N + 127) / 128) < big / 16;
 }
 
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+AttendPlan make_plan(int64_t B, int64_t Sq, int64_t Hq, int64_t Hkv, int64_t N, int64_t D) {
+    AttendPlan p{};
+    const int64_t R = Sq * (Hq / Hkv), bh = B * Hkv;
+    p.rt = R <= 16 ? 16 : R <= 32 ? 32 : 64;
+    p.row_tiles = (int)((R + p.rt - 1) / p.rt);
+    const int subs = (int)(D + 63) / 64, stage = subs * kTile * 128, o_cols = (int)(D + 127) / 128 * p.rt;
+    // two blocks an SM where rows and weights leave room for three stages in half of it
+    const int fixed = subs * p.rt * 128 + p.rt * 512 + 1024;
+    const bool two = fixed + 3 * stage <= 112 * 1024;
+    p.cols = two ? 256 : 512;
+    // one block of 64 columns more than the ring holds may be read as (unused) rows of V^T
+    const int room = (two ? 112 : 224) * 1024 - fixed;
+    p.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
+    p.smem = p.stages * stage + fixed + (subs % 2 ? kTile * 128 : 0);
+    while (p.smem > (two ? 112 : 224) * 1024) {
+        --p.stages;
+        p.smem -= stage;
+    }
+    const int cap = (p.cols - o_cols) / p.rt;
+    const int64_t tiles = (N + kTile - 1) / kTile;
+    const int64_t most = cap < kMaxTiles ? cap : kMaxTiles;
+    int64_t splits = (tiles + most - 1) / most;
+    // enough blocks to fill 148 SMs
+    const int64_t want = (148 * (two ? 2 : 1) + bh * p.row_tiles - 1) / (bh * p.row_tiles);
+    if (splits < want) splits = want < tiles ? want : tiles;
+    p.splits = (int)splits;
+    p.tiles = (int)((tiles + splits - 1) / splits);
+    p.RP = (R + 3) / 4 * 4;
+    p.off_part = up256((size_t)(bh * splits * R) * 8);
+    p.off_logits = p.off_part + up256((size_t)(bh * splits * R) * (size_t)D * 4);
+    p.bytes = p.off_logits + up256((size_t)(bh * N) * (size_t)p.RP * 4);
+    return p;
+}
+
+// The driver's tensor-map encoder, looked up once.
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+    static std::atomic<void*> fn{nullptr};
+    void* f = fn.load(std::memory_order_acquire);
+    if (f == nullptr) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn.store(f, std::memory_order_release);
+    }
+    return (EncodeFn)f;
+}
+
+// A cache as (B, Hkv, N, D), boxes of 128 rows by 64 elements, swizzled by 128 bytes.  A
+// dimension that repeats one and the same memory (stride 0) is mapped with length 1.
+bool cache_map(CUtensorMap* map, int dtype, const void* base, int64_t B, int64_t H, int64_t N,
+               int64_t D, int64_t sb, int64_t sh, int64_t sr, int* use_h, int* use_b) {
+    const EncodeFn encode = encoder();
+    if (encode == nullptr) return false;
+    *use_h = sh > 0 && H > 1;
+    *use_b = sb > 0 && B > 1;
+    const int64_t rows = sr > 0 ? N : 1;
+    if (rows < N) return false;  // every row the same memory: not a cache
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)N, (cuuint64_t)(*use_h ? H : 1),
+                                (cuuint64_t)(*use_b ? B : 1)};
+    const cuuint64_t strides[3] = {(cuuint64_t)sr * 2, (cuuint64_t)(*use_h ? sh : sr) * 2,
+                                   (cuuint64_t)(*use_b ? sb : sr) * 2};
+    const cuuint32_t box[4] = {64, kTile, 1, 1}, step[4] = {1, 1, 1, 1};
+    return encode(map, dtype == LAPSUM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                  : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  4, const_cast<void*>(base), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, int RT>
+cudaError_t launch_split(const AttendArgs& a, const AttendPlan& p, const void* q,
+                         const CUtensorMap& k, const CUtensorMap& v, float2* stats, float* part,
+                         float* logits, cudaStream_t st) {
+    static std::atomic<unsigned long long> done{0};
+    once_per_device(done, [] {
+        cudaFuncSetAttribute(attend_split_kernel<T, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             225 * 1024);
+    });
+    const int64_t blocks = (int64_t)a.B * a.Hkv * p.splits * p.row_tiles;
+    return launch_pdl(attend_split_kernel<T, RT>, dim3((unsigned)blocks), dim3(kSplitThreads),
+                      (size_t)p.smem, st, a, p, (const T*)q, k, v, stats, part, logits);
+}
+
+template <class T>
+cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& p, const void* q,
+                          const CUtensorMap& k, const CUtensorMap& v, char* ws,
+                          const float* score_in, float* score_out, void* out, cudaStream_t st) {
+    float2* stats = (float2*)ws;
+    float* part = (float*)(ws + p.off_part);
+    float* logits = (float*)(ws + p.off_logits);
+    cudaError_t e;
+    {
+        ProfScope prof("attend_split", st);
+        e = p.rt == 16   ? launch_split<T, 16>(a, p, q, k, v, stats, part, logits, st)
+            : p.rt == 32 ? launch_split<T, 32>(a, p, q, k, v, stats, part, logits, st)
+                         : launch_split<T, 64>(a, p, q, k, v, stats, part, logits, st);
+    }
+    if (e != cudaSuccess) return e;
+    ProfScope prof("attend_join", st);
+    const int key_blocks = (int)((a.N + kJoinThreads - 1) / kJoinThreads);
+    const int64_t score_blocks = (int64_t)a.B * a.Hkv * key_blocks;
+    const int64_t rows = (int64_t)a.B * a.Hkv * a.R;
+    return launch_pdl(attend_join_kernel<T>, dim3((unsigned)(score_blocks + (rows + 7) / 8)),
+                      dim3(kJoinThreads), 0, st, a, p, score_blocks, key_blocks,
+                      (const float2*)stats, (const float*)part, (const float*)logits, score_in,
+                      score_out, (T*)out);
+}
 
 }  // namespace
 }  // namespace lapsum
@@ -117,7 +621,7 @@ using namespace lapsum;
 extern "C" size_t lapsum_attend_workspace_bytes(int64_t B, int64_t Sq, int64_t Hq, int64_t Hkv,
                                                 int64_t N, int64_t D) {
     if (!attend_sizes_ok(B, Sq, Hq, Hkv, N, D)) return 0;
-    return up256((size_t)(B * Sq * Hq) * 4) + up256((size_t)(B * Sq * Hq) * (size_t)N * 4);
+    return make_plan(B, Sq, Hq, Hkv, N, D).bytes;
 }
 
 extern "C" int lapsum_attend_accumulate(const void* q, const void* k, const void* v, int dtype,
@@ -132,44 +636,42 @@ extern "C" int lapsum_attend_accumulate(const void* q, const void* k, const void
     if (!attend_sizes_ok(B, Sq, Hq, Hkv, N, D) || !std::isfinite(scale)) return LAPSUM_EINVAL;
     for (int i = 0; i < 13; ++i)
         if (strides[i] < 0 || (i < 9 && strides[i] % 8 != 0)) return LAPSUM_EINVAL;
+    // rows of one cache may repeat over heads and sequences, but not over its keys
+    if (N > 1 && (strides[5] < D || strides[8] < D)) return LAPSUM_EINVAL;
     if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(out, 16) ||
         !aligned_to(lengths, 4) || !aligned_to(score_in, 4) || !aligned_to(score_out, 4))
         return LAPSUM_EINVAL;
-    if (ws == nullptr || !aligned_to(ws, 256) ||
-        ws_bytes < lapsum_attend_workspace_bytes(B, Sq, Hq, Hkv, N, D))
-        return LAPSUM_EWORKSPACE;
-    AttendArgs a;
-    int64_t* s = &a.qb;
-    for (int i = 0; i < 13; ++i) s[i] = strides[i];
-    a.B = B;
-    a.Sq = Sq;
-    a.Hq = Hq;
-    a.Hkv = Hkv;
+    const AttendPlan p = make_plan(B, Sq, Hq, Hkv, N, D);
+    if (ws == nullptr || !aligned_to(ws, 256) || ws_bytes < p.bytes) return LAPSUM_EWORKSPACE;
+    AttendArgs a{};
+    a.qb = strides[0];
+    a.qh = strides[1];
+    a.qr = strides[2];
+    a.sib = strides[9];
+    a.sih = strides[10];
+    a.sob = strides[11];
+    a.soh = strides[12];
     a.N = N;
+    a.B = (int)B;
+    a.Sq = (int)Sq;
+    a.Hkv = (int)Hkv;
     a.D = (int)D;
     a.G = (int)(Hq / Hkv);
-    a.scale = scale;
+    a.R = Sq * a.G;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634);
     a.lengths = lengths;
+    CUtensorMap k_map, v_map;
+    const int64_t row = D < 8 ? 8 : D;  // a row stride for caches of one row
+    if (!cache_map(&k_map, dtype, k, B, Hkv, N, D, strides[3], strides[4],
+                   N > 1 ? strides[5] : row, &a.kh, &a.kb) ||
+        !cache_map(&v_map, dtype, v, B, Hkv, N, D, strides[6], strides[7],
+                   N > 1 ? strides[8] : row, &a.vh, &a.vb))
+        return LAPSUM_ECUDA;
     cudaStream_t st = (cudaStream_t)stream;
-    float* lse = (float*)ws;
-    float* logits = (float*)((char*)ws + up256((size_t)(B * Sq * Hq) * 4));
-    cudaError_t e;
-    {
-        ProfScope prof("attend_rows", st);
-        e = with_dtype(dtype, [&](auto* tag) {
-            using T = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
-            return launch_pdl(attend_rows_kernel<T>, dim3((unsigned)(B * Sq * Hq)),
-                              dim3(kAttThreads), 0, st, a, (const T*)q, (const T*)k, (const T*)v,
-                              (T*)out, logits, lse);
-        });
-    }
-    if (e != cudaSuccess) return LAPSUM_ECUDA;
-    ProfScope prof("attend_score", st);
-    const int64_t blocks = (N + kAttThreads - 1) / kAttThreads, bh = B * Hkv;
-    const unsigned gy = (unsigned)(bh < 32768 ? bh : 32768);
-    e = launch_pdl(attend_score_kernel,
-                   dim3((unsigned)(blocks < 1024 ? blocks : 1024), gy, (unsigned)((bh + gy - 1) / gy)),
-                   dim3(kAttThreads), 0, st, a, (const float*)logits, (const float*)lse, score_in,
-                   score_out);
+    const cudaError_t e =
+        dtype == LAPSUM_DTYPE_BF16
+            ? launch_attend<__nv_bfloat16>(a, p, q, k_map, v_map, (char*)ws, score_in, score_out,
+                                           out, st)
+            : launch_attend<__half>(a, p, q, k_map, v_map, (char*)ws, score_in, score_out, out, st);
     return e == cudaSuccess ? LAPSUM_OK : LAPSUM_ECUDA;
 }
