@@ -3,10 +3,17 @@
 // scores stay, `budget` in all, in the order of their positions.  Entry point:
 // lapsum_evict (include/lapsum.h).
 //
-// Selection: one block per row finds the exact boundary score by radix selection
-// over order-preserving integer keys, then walks the row once and writes the kept
-// positions in order; equal scores at the boundary go to the lowest positions.
+// Selection, one block per row.  Scores become order-preserving integer keys.  A
+// sample of the row gives a range [lo, hi] of keys that holds the boundary key with
+// high probability (the bracketing of section 2.2 of the pages, on order statistics
+// of plain samples); one pass over the row then marks the keys above the range in a bit map
+// and lists those inside, and the boundary is found in the list by radix selection.
+// Counts prove the range right; where they do not, or where the list would
+// overflow, histogram passes over the row narrow the range first.  The kept positions
+// come out of the bit map in order, so nothing is sorted; keys equal to the boundary
+// have a bit map of their own, of which the first (lowest positions) are taken.
 // Gathering: one thread per 16 bytes of a kept row, over all rows at once.
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -19,6 +26,11 @@ namespace {
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBits = 11, kSelBins = 1 << kSelBits;
+constexpr int kSelSample = 2048;
+constexpr int kSelList = 8192;
+constexpr int64_t kSelWindow = int64_t(1) << 18;  // positions that the bit maps hold at a time
+static_assert(kSelSample <= kSelBins, "the sample is sorted where the histogram stands");
 constexpr unsigned kAll = 0xffffffffu;
 
 struct EvictArgs {
@@ -40,7 +52,7 @@ __device__ __forceinline__ int64_t row_length(const EvictArgs& a, int64_t b) {
     return n < 0 ? 0 : n > a.N ? a.N : n;
 }
 
-// Exclusive block-wide prefix sum of two counts packed in one word pair.
+// Exclusive block-wide prefix sum of a pair of counts; *tot gets the totals.
 __device__ __forceinline__ int2 block_prefix(int2 v, int2* tot, int2* sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int2 inc = v;
@@ -56,6 +68,7 @@ __device__ __forceinline__ int2 block_prefix(int2 v, int2* tot, int2* sums) {
     if (lane == 31) sums[warp] = inc;
     __syncthreads();
     int2 before = make_int2(0, 0), all = make_int2(0, 0);
+#pragma unroll
     for (int w = 0; w < kSelWarps; ++w) {
         const int2 s = sums[w];
         if (w < warp) {
@@ -69,13 +82,154 @@ __device__ __forceinline__ int2 block_prefix(int2 v, int2* tot, int2* sums) {
     return make_int2(before.x + inc.x - v.x, before.y + inc.y - v.y);
 }
 
+// What the block knows about its row's boundary: it is the need-th largest key of the
+// competitors, `above` of them lie above hi and `inside` in [lo, hi].
+struct Range {
+    uint32_t lo, hi;
+    int64_t above, inside;
+};
+
+struct SelShared {
+    unsigned hist[kSelBins];  // also the sorted sample
+    int2 sums[kSelWarps];
+    Range range;
+    int listed;               // keys listed (may exceed the room)
+    unsigned long long above;
+};
+
+// Bin of a key of [lo, hi] when the range is cut into at most kSelBins bins.
+__device__ __forceinline__ int range_shift(uint32_t lo, uint32_t hi) {
+    const int bits = 32 - __clz(hi - lo);  // 0 for a single key
+    return bits > kSelBits ? bits - kSelBits : 0;
+}
+
+// Adds one to a bin; a warp whose active lanes all want the same bin adds once.
+__device__ __forceinline__ void count_bin(unsigned* hist, int bin) {
+    const unsigned on = __activemask();
+    int same;
+    __match_all_sync(on, bin, &same);
+    if (same) {
+        if ((threadIdx.x & 31) == __ffs(on) - 1) atomicAdd(&hist[bin], (unsigned)__popc(on));
+    } else {
+        atomicAdd(&hist[bin], 1u);
+    }
+}
+
+// Narrows the range to the bin that holds the need-th largest key.  The histogram of
+// the keys inside the range is complete; every thread calls.
+__device__ void narrow_range(SelShared& sh, int64_t need) {
+    __syncthreads();
+    const Range g = sh.range;
+    const int shift = range_shift(g.lo, g.hi);
+    // thread t owns kSelBins / kSelThreads bins, highest first
+    constexpr int kOwn = kSelBins / kSelThreads;
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) mine += sh.hist[kSelBins - 1 - (threadIdx.x * kOwn + i)];
+    int2 tot;
+    int64_t at = g.above + block_prefix(make_int2(mine, 0), &tot, sh.sums).x;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        const int bin = kSelBins - 1 - (threadIdx.x * kOwn + i);
+        const int64_t c = sh.hist[bin];
+        if (at < need && need <= at + c) {
+            const uint32_t lo = g.lo + ((uint32_t)bin << shift);
+            const uint64_t hi = (uint64_t)lo + (1ull << shift) - 1;
+            sh.range = Range{lo, hi < g.hi ? (uint32_t)hi : g.hi, at, c};
+        }
+        at += c;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void clear_words(uint32_t* w, int64_t n) {
+    for (int64_t i = threadIdx.x; i < n; i += kSelThreads) w[i] = 0;
+}
+
+// Calls f(position, key) for this thread's share of the positions [lo, hi), which is four
+// consecutive ones at a time.
+template <class F>
+__device__ __forceinline__ void each_key(const float* score, int64_t lo, int64_t hi, F f) {
+    // up to the first 16-byte boundary and from the last on, one at a time
+    const int64_t skew = (int64_t)((reinterpret_cast<uintptr_t>(score + lo) & 15u) / 4);
+    int64_t head = lo + (skew ? 4 - skew : 0);
+    if (head > hi) head = hi;
+    const int64_t quads = (hi - head) / 4, tail = head + quads * 4;
+    if (threadIdx.x < head - lo) f(lo + threadIdx.x, score_key(score[lo + threadIdx.x]));
+    if (threadIdx.x < hi - tail) f(tail + threadIdx.x, score_key(score[tail + threadIdx.x]));
+    const float4* s4 = reinterpret_cast<const float4*>(score + head);
+    constexpr int kUnroll = 4;
+    int64_t i = threadIdx.x;
+    for (; i + (kUnroll - 1) * kSelThreads < quads; i += kUnroll * kSelThreads) {
+        float4 v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) v[u] = __ldg(s4 + i + u * kSelThreads);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t at = head + (i + u * kSelThreads) * 4;
+            f(at, score_key(v[u].x));
+            f(at + 1, score_key(v[u].y));
+            f(at + 2, score_key(v[u].z));
+            f(at + 3, score_key(v[u].w));
+        }
+    }
+    for (; i < quads; i += kSelThreads) {
+        const float4 v = __ldg(s4 + i);
+        const int64_t at = head + i * 4;
+        f(at, score_key(v.x));
+        f(at + 1, score_key(v.y));
+        f(at + 2, score_key(v.z));
+        f(at + 3, score_key(v.w));
+    }
+}
+
+// A sample of the competitors brackets the boundary: sorted in shared memory, its
+// order statistics 3.5 standard deviations either side of the expected rank.
+__device__ void sample_range(SelShared& sh, const float* score, int64_t lo, int64_t hi,
+                             int64_t need) {
+    const int64_t n = hi - lo;
+    for (int i = threadIdx.x; i < kSelSample; i += kSelThreads) {
+        // one draw from each of kSelSample equal stretches
+        uint32_t x = (uint32_t)i * 0x9e3779b9u;
+        x ^= x >> 15;
+        x *= 0x85ebca6bu;
+        x ^= x >> 13;
+        const int64_t a = n * i / kSelSample, b = n * (i + 1) / kSelSample;
+        sh.hist[i] = score_key(score[lo + a + (int64_t)(x % (uint32_t)(b - a))]);
+    }
+    for (int size = 2; size <= kSelSample; size <<= 1)
+        for (int step = size >> 1; step > 0; step >>= 1) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < kSelSample / 2; i += kSelThreads) {
+                const int at = 2 * i - (i & (step - 1)), to = at + step;
+                const unsigned u = sh.hist[at], v = sh.hist[to];
+                if ((u < v) == ((at & size) == 0)) {  // descending overall
+                    sh.hist[at] = v;
+                    sh.hist[to] = u;
+                }
+            }
+        }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const double q = (double)need / (double)n, mean = q * kSelSample;
+        const double sd = sqrt(mean * (1.0 - q));
+        const double up = mean - 3.5 * sd - 2.0, down = mean + 3.5 * sd + 2.0;
+        sh.range = Range{down < kSelSample ? sh.hist[(int)down] : 0u,
+                         up >= 0.0 ? sh.hist[(int)up] : 0xffffffffu, 0, 0};
+    }
+    __syncthreads();
+}
+
 __global__ void __launch_bounds__(kSelThreads)
-    evict_select_kernel(EvictArgs a, int32_t* positions, int32_t* lengths_out) {
+    evict_select_kernel(EvictArgs a, int64_t window, int32_t* positions, int32_t* lengths_out) {
     pdl_wait();
-    __shared__ unsigned hist[256];
-    __shared__ int2 sums[kSelWarps];
-    __shared__ uint32_t s_prefix;
-    __shared__ int64_t s_need;
+    extern __shared__ uint32_t sel_smem[];
+    __shared__ SelShared sh;
+    uint32_t* list_key = sel_smem;                  // [kSelList]
+    int32_t* list_at = (int32_t*)(sel_smem + kSelList);
+    uint32_t* above_map = sel_smem + 2 * kSelList;  // a bit per position of a window
+    uint32_t* tie_map = above_map + window / 32;
+    const int lane = threadIdx.x & 31;
     const int64_t r = blockIdx.x, b = r / a.H, h = r - b * a.H;
     const int64_t n = row_length(a, b);
     const float* score = a.score + b * a.score_b + h * a.score_h;
@@ -87,54 +241,162 @@ __global__ void __launch_bounds__(kSelThreads)
         for (int64_t i = threadIdx.x; i < n; i += kSelThreads) pos[i] = (int32_t)i;
         return;
     }
-    const int64_t lo = a.first, hi = n - a.last;  // the keys that compete
-    if (threadIdx.x == 0) {
-        s_prefix = 0;
-        s_need = a.budget - a.first - a.last;
-    }
-    // the key of the need-th largest competitor, eight bits at a time
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        const uint32_t prefix = s_prefix;
-        const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-        for (int64_t i = lo + threadIdx.x; i < hi; i += kSelThreads) {
-            const uint32_t key = score_key(score[i]);
-            if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+    const int64_t lo = a.first, hi = n - a.last;  // the positions that compete
+    const int64_t need = a.budget - a.first - a.last;
+    const bool one = n <= window;                 // the whole row fits the bit maps
+    bool marked = false;                          // they are filled
+    bool listed = false;                          // the list holds the range's keys
+    if (need > 0) {
+        if (hi - lo <= kSelList) {
+            if (threadIdx.x == 0) sh.range = Range{0u, 0xffffffffu, 0, hi - lo};
+            __syncthreads();
+        } else {
+            sample_range(sh, score, lo, hi, need);
         }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            int64_t need = s_need;
-            int d = 255;
-            for (; d > 0 && (int64_t)hist[d] < need; --d) need -= hist[d];
-            s_need = need;
-            s_prefix = prefix | ((uint32_t)d << shift);
+        bool known = hi - lo <= kSelList;  // the range's counts are exact
+        // One pass marks and lists; when the range proves wrong or too full, histogram
+        // passes narrow it until the list holds it, or until it is one key.
+        for (;;) {
+            const Range g = sh.range;
+            if (known && g.lo == g.hi) break;
+            if (!known || g.inside <= kSelList) {
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    sh.listed = 0;
+                    sh.above = 0;
+                }
+                if (one) {
+                    clear_words(above_map, (n + 31) / 32);
+                    clear_words(tie_map, (n + 31) / 32);
+                }
+                __syncthreads();
+                unsigned over = 0;
+                each_key(score, lo, hi, [&](int64_t at, uint32_t key) {
+                    if (key < g.lo) return;
+                    if (key > g.hi) {
+                        ++over;
+                        if (one) atomicOr(&above_map[at >> 5], 1u << (at & 31));
+                        return;
+                    }
+                    const unsigned on = __activemask();
+                    const int lead = __ffs(on) - 1;
+                    int base = 0;
+                    if (lane == lead) base = atomicAdd(&sh.listed, __popc(on));
+                    base = __shfl_sync(on, base, lead) + __popc(on & ((1u << lane) - 1u));
+                    if (base < kSelList) {
+                        list_key[base] = key;
+                        list_at[base] = (int32_t)at;
+                    }
+                });
+                if (over) atomicAdd(&sh.above, (unsigned long long)over);
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    sh.range.above = (int64_t)sh.above;
+                    sh.range.inside = sh.listed;
+                }
+                __syncthreads();
+                const Range e = sh.range;
+                if (e.above < need && need <= e.above + e.inside) {
+                    known = true;
+                    listed = e.inside <= kSelList;
+                    if (listed) break;
+                } else {  // the sample missed
+                    __syncthreads();
+                    if (threadIdx.x == 0) sh.range = Range{0u, 0xffffffffu, 0, hi - lo};
+                    __syncthreads();
+                    known = true;
+                }
+                continue;
+            }
+            for (int i = threadIdx.x; i < kSelBins; i += kSelThreads) sh.hist[i] = 0;
+            __syncthreads();
+            const int shift = range_shift(g.lo, g.hi);
+            each_key(score, lo, hi, [&](int64_t, uint32_t key) {
+                if (key >= g.lo && key <= g.hi) count_bin(sh.hist, (int)((key - g.lo) >> shift));
+            });
+            narrow_range(sh, need);
         }
-        __syncthreads();
-    }
-    const uint32_t cut = s_prefix;
-    const int64_t ties = s_need;  // how many competitors equal to the cut stay
-    int64_t out = 0, tied = 0;
-    for (int64_t base = 0; base < n; base += kSelThreads) {
-        const int64_t i = base + threadIdx.x;
-        bool keep = false, tie = false;
-        if (i < n) {
-            if (i < lo || i >= hi) keep = true;
-            else {
-                const uint32_t key = score_key(score[i]);
-                keep = key > cut;
-                tie = key == cut;
+        if (listed) {
+            const int m = (int)sh.range.inside;
+            while (sh.range.lo != sh.range.hi) {
+                const Range g = sh.range;
+                __syncthreads();
+                for (int i = threadIdx.x; i < kSelBins; i += kSelThreads) sh.hist[i] = 0;
+                __syncthreads();
+                const int shift = range_shift(g.lo, g.hi);
+                for (int i = threadIdx.x; i < m; i += kSelThreads) {
+                    const uint32_t key = list_key[i];
+                    if (key >= g.lo && key <= g.hi) count_bin(sh.hist, (int)((key - g.lo) >> shift));
+                }
+                narrow_range(sh, need);
+            }
+            if (one) {
+                const uint32_t cut = sh.range.lo;
+                for (int i = threadIdx.x; i < m; i += kSelThreads) {
+                    const uint32_t key = list_key[i];
+                    const int32_t at = list_at[i];
+                    if (key > cut) atomicOr(&above_map[at >> 5], 1u << (at & 31));
+                    if (key == cut) atomicOr(&tie_map[at >> 5], 1u << (at & 31));
+                }
+                marked = true;
             }
         }
-        int2 tot;
-        const int2 at = block_prefix(make_int2(keep, tie), &tot, sums);
-        // kept so far = kept outright + the ties among the first `ties`
-        const int64_t tie_at = tied + at.y;
-        const int64_t taken = (tie_at < ties ? tie_at : ties) - (tied < ties ? tied : ties);
-        if (keep || (tie && tie_at < ties)) pos[out + at.x + taken] = (int32_t)i;
-        const int64_t t2 = tied + tot.y;
-        out += tot.x + (t2 < ties ? t2 : ties) - (tied < ties ? tied : ties);
-        tied = t2;
+    }
+    __syncthreads();
+    const uint32_t cut = need > 0 ? sh.range.lo : 0xffffffffu;
+    const int64_t ties = need > 0 ? need - sh.range.above : 0;  // competitors at the cut that stay
+    // out of the bit maps, a window of positions at a time
+    int64_t out = 0, tied = 0;
+    for (int64_t w0 = 0; w0 < n; w0 += window) {
+        const int64_t w1 = w0 + window < n ? w0 + window : n;
+        const int words = (int)((w1 - w0 + 31) / 32);
+        if (!marked) {
+            __syncthreads();
+            clear_words(above_map, words);
+            clear_words(tie_map, words);
+            __syncthreads();
+            if (need > 0)
+                each_key(score, lo < w0 ? w0 : lo < w1 ? lo : w1, hi < w0 ? w0 : hi < w1 ? hi : w1,
+                         [&](int64_t at, uint32_t key) {
+                             const int i = (int)(at - w0);
+                             if (key > cut) atomicOr(&above_map[i >> 5], 1u << (i & 31));
+                             if (key == cut) atomicOr(&tie_map[i >> 5], 1u << (i & 31));
+                         });
+            __syncthreads();
+        }
+        for (int base = 0; base < words; base += kSelThreads) {
+            const int i = base + threadIdx.x;
+            uint32_t A = 0, T = 0;
+            if (i < words) {
+                A = above_map[i];
+                T = tie_map[i];
+                // the first and the last stay whatever their scores
+                const int64_t p0 = w0 + (int64_t)i * 32;
+                const int64_t c = lo - p0, d = hi - p0;
+                if (c > 0) A |= c >= 32 ? kAll : (1u << c) - 1u;
+                if (d < 32) A |= d <= 0 ? kAll : kAll << d;
+                if (n - p0 < 32) A &= (1u << (n - p0)) - 1u;
+            }
+            int2 tot;
+            const int2 at = block_prefix(make_int2(__popc(A), __popc(T)), &tot, sh.sums);
+            // kept before this word: its A bits and the ties among the first `ties`
+            const int64_t t0 = tied + at.y;
+            const int64_t was = tied < ties ? tied : ties;
+            int64_t o = out + at.x + ((t0 < ties ? t0 : ties) - was);
+            int64_t left = ties - t0;
+            uint32_t bits = A | T;
+            while (bits) {
+                const int k = __ffs(bits) - 1;
+                bits &= bits - 1;
+                if ((T >> k) & 1u) {
+                    if (left-- <= 0) continue;
+                }
+                pos[o++] = (int32_t)(w0 + (int64_t)i * 32 + k);
+            }
+            const int64_t t2 = tied + tot.y;
+            out += tot.x + ((t2 < ties ? t2 : ties) - was);
+            tied = t2;
+        }
     }
 }
 
@@ -209,8 +471,14 @@ extern "C" int lapsum_evict(const void* k, const void* v, int dtype, const float
     cudaError_t e;
     {
         ProfScope prof("evict_select", st);
-        e = launch_pdl(evict_select_kernel, dim3((unsigned)a.rows), dim3(kSelThreads), 0, st, a,
-                       positions, lengths_out);
+        static std::atomic<unsigned long long> done{0};
+        const int64_t window = N < kSelWindow ? (N + 31) / 32 * 32 : kSelWindow;
+        once_per_device(done, [] {
+            cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(kSelList * 8 + kSelWindow / 4));
+        });
+        e = launch_pdl(evict_select_kernel, dim3((unsigned)a.rows), dim3(kSelThreads),
+                       (size_t)(kSelList * 8 + window / 4), st, a, window, positions, lengths_out);
     }
     if (e != cudaSuccess) return LAPSUM_ECUDA;
     ProfScope prof("evict_gather", st);

@@ -224,6 +224,41 @@ def test_evict(cuda_device, kind, B, H, N, D, budget, first, last):
         check_evict(k, v, s, [max(1, N - 37 * b) for b in range(B)], budget, first, last)
 
 
+@pytest.mark.parametrize("n,budget,kind", [
+    (9000, 4000, "normal"), (70001, 1024, "normal"), (70001, 35000, "normal"), (70001, 69990, "small"),
+    (70001, 3, "ties"), (70001, 30000, "same"), (70001, 20000, "ties"), (300000, 70000, "normal"),
+    (300000, 500, "ties"), (600001, 300000, "small"), (600001, 20, "same"), (70001, 9, "hidden"),
+    (300000, 9, "hidden")])
+def test_evict_long_rows(cuda_device, n, budget, kind):
+    """Rows beyond the list and beyond one window of the bit maps, with samples that
+    bracket, that miss (a few large scores among equal ones) and that hold too many ties:
+    positions against numpy's stable sort."""
+    gen = torch.Generator().manual_seed(n + budget)
+    s = torch.randn((1, 2, n + 3), generator=gen)
+    if kind == "ties":
+        s = (s * 2).round() / 2
+    if kind == "small":
+        s = (s * 5 - 20).exp()
+    if kind == "same":
+        s = torch.ones_like(s)
+    if kind == "hidden":
+        s = torch.full_like(s, 0.25)
+        s[0, 0, 5000:5006] = 2.0
+        s[0, 1, -40:-20] = torch.arange(20) + 1.0
+    s = s.cuda()[:, :, 3:]      # rows off a 16-byte boundary
+    first, last = (2, 5) if budget > 8 else (0, 0)
+    k = torch.randn((1, 2, n, 8), generator=gen).to(torch.bfloat16).cuda()
+    e = L.evict(k, k.clone(), s, torch.tensor([n], dtype=torch.int32).cuda(), budget, first=first, last=last)
+    for h in range(2):
+        x = s[0, h].cpu().numpy().astype(np.float64)
+        x[:first] = np.inf
+        x[n - last:] = np.inf
+        want = np.sort(np.argsort(-x, kind="stable")[:budget])
+        assert np.array_equal(e.positions[0, h].cpu().numpy(), want)
+        at = torch.from_numpy(want).cuda()
+        assert torch.equal(e.k[0, h], k[0, h, at]) and torch.equal(e.score[0, h], s[0, h, at])
+
+
 def test_evict_short_rows(cuda_device):
     """Lengths of zero, one, the budget and one more; lengths beyond N and below 0."""
     k, v, s = evict_inputs(1, 7, 2, 64, 32, torch.float16)
