@@ -17,6 +17,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "bitonic.cuh"
 #include "elements.cuh"
 #include "lapsum_common.cuh"
 #include "lapsum_kernels.h"
@@ -27,10 +28,10 @@ namespace {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBits = 11, kSelBins = 1 << kSelBits;
-constexpr int kSelSample = 2048;
+constexpr int kSelSample = 2 * kSelThreads;
 constexpr int kSelList = 8192;
 constexpr int64_t kSelWindow = int64_t(1) << 18;  // positions that the bit maps hold at a time
-static_assert(kSelSample <= kSelBins, "the sample is sorted where the histogram stands");
+static_assert(kSelSample <= kSelList, "the sample is sorted where the list will stand");
 constexpr unsigned kAll = 0xffffffffu;
 
 struct EvictArgs {
@@ -86,15 +87,15 @@ __device__ __forceinline__ int2 block_prefix(int2 v, int2* tot, int2* sums) {
 // competitors, `above` of them lie above hi and `inside` in [lo, hi].
 struct Range {
     uint32_t lo, hi;
-    int64_t above, inside;
+    int above, inside;
 };
 
 struct SelShared {
-    unsigned hist[kSelBins];  // also the sorted sample
+    alignas(16) unsigned hist[kSelBins];
     int2 sums[kSelWarps];
     Range range;
     int listed;               // keys listed (may exceed the room)
-    unsigned long long above;
+    int above;
 };
 
 // Bin of a key of [lo, hi] when the range is cut into at most kSelBins bins.
@@ -117,27 +118,25 @@ __device__ __forceinline__ void count_bin(unsigned* hist, int bin) {
 
 // Narrows the range to the bin that holds the need-th largest key.  The histogram of
 // the keys inside the range is complete; every thread calls.
-__device__ void narrow_range(SelShared& sh, int64_t need) {
+__device__ void narrow_range(SelShared& sh, int need) {
     __syncthreads();
     const Range g = sh.range;
     const int shift = range_shift(g.lo, g.hi);
-    // thread t owns kSelBins / kSelThreads bins, highest first
-    constexpr int kOwn = kSelBins / kSelThreads;
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) mine += sh.hist[kSelBins - 1 - (threadIdx.x * kOwn + i)];
+    // thread t owns four neighbouring bins, the highest ones first
+    static_assert(kSelBins == 4 * kSelThreads, "four bins a thread");
+    const int bin0 = kSelBins - 4 - 4 * (int)threadIdx.x;
+    const uint4 q = *reinterpret_cast<const uint4*>(&sh.hist[bin0]);
+    const int c[4] = {(int)q.w, (int)q.z, (int)q.y, (int)q.x};
     int2 tot;
-    int64_t at = g.above + block_prefix(make_int2(mine, 0), &tot, sh.sums).x;
+    int at = g.above + block_prefix(make_int2(c[0] + c[1] + c[2] + c[3], 0), &tot, sh.sums).x;
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-        const int bin = kSelBins - 1 - (threadIdx.x * kOwn + i);
-        const int64_t c = sh.hist[bin];
-        if (at < need && need <= at + c) {
-            const uint32_t lo = g.lo + ((uint32_t)bin << shift);
+    for (int i = 0; i < 4; ++i) {
+        if (at < need && need <= at + c[i]) {
+            const uint32_t lo = g.lo + ((uint32_t)(bin0 + 3 - i) << shift);
             const uint64_t hi = (uint64_t)lo + (1ull << shift) - 1;
-            sh.range = Range{lo, hi < g.hi ? (uint32_t)hi : g.hi, at, c};
+            sh.range = Range{lo, hi < g.hi ? (uint32_t)hi : g.hi, at, c[i]};
         }
-        at += c;
+        at += c[i];
     }
     __syncthreads();
 }
@@ -183,44 +182,130 @@ __device__ __forceinline__ void each_key(const float* score, int64_t lo, int64_t
     }
 }
 
-// A sample of the competitors brackets the boundary: sorted in shared memory, its
-// order statistics 3.5 standard deviations either side of the expected rank.
-__device__ void sample_range(SelShared& sh, const float* score, int64_t lo, int64_t hi,
-                             int64_t need) {
+// A sample of the competitors brackets the boundary: two keys a thread, sorted across
+// the block, and the order statistics 3.5 standard deviations either side of the expected
+// rank.  `sorted` holds kSelSample words.
+__device__ void sample_range(SelShared& sh, uint32_t* sorted, const float* score, int64_t lo,
+                             int64_t hi, int64_t need) {
     const int64_t n = hi - lo;
-    for (int i = threadIdx.x; i < kSelSample; i += kSelThreads) {
-        // one draw from each of kSelSample equal stretches
-        uint32_t x = (uint32_t)i * 0x9e3779b9u;
-        x ^= x >> 15;
-        x *= 0x85ebca6bu;
-        x ^= x >> 13;
-        const int64_t a = n * i / kSelSample, b = n * (i + 1) / kSelSample;
-        sh.hist[i] = score_key(score[lo + a + (int64_t)(x % (uint32_t)(b - a))]);
-    }
-    for (int size = 2; size <= kSelSample; size <<= 1)
-        for (int step = size >> 1; step > 0; step >>= 1) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < kSelSample / 2; i += kSelThreads) {
-                const int at = 2 * i - (i & (step - 1)), to = at + step;
-                const unsigned u = sh.hist[at], v = sh.hist[to];
-                if ((u < v) == ((at & size) == 0)) {  // descending overall
-                    sh.hist[at] = v;
-                    sh.hist[to] = u;
-                }
-            }
-        }
+    // four neighbours (one memory sector, mostly) from each of kSelSample / 4 equal
+    // stretches; two threads share them
+    const int stretch = threadIdx.x >> 1;
+    uint32_t x = (uint32_t)stretch * 0x9e3779b9u;
+    x ^= x >> 15;
+    x *= 0x85ebca6bu;
+    x ^= x >> 13;
+    const int64_t a = n * stretch / (kSelSample / 4), b = n * (stretch + 1) / (kSelSample / 4);
+    const float* at = score + lo + a + (int64_t)(x % (uint32_t)(b - a - 3)) + (threadIdx.x & 1) * 2;
+    uint32_t v[2] = {score_key(at[0]), score_key(at[1])};
+    bitonic_sort_row<2, kSelThreads, kSelThreads>(v, threadIdx.x, sorted);
+    sorted[kSelSample - 1 - 2 * threadIdx.x] = v[0];  // descending
+    sorted[kSelSample - 2 - 2 * threadIdx.x] = v[1];
     __syncthreads();
     if (threadIdx.x == 0) {
         const double q = (double)need / (double)n, mean = q * kSelSample;
         const double sd = sqrt(mean * (1.0 - q));
         const double up = mean - 3.5 * sd - 2.0, down = mean + 3.5 * sd + 2.0;
-        sh.range = Range{down < kSelSample ? sh.hist[(int)down] : 0u,
-                         up >= 0.0 ? sh.hist[(int)up] : 0xffffffffu, 0, 0};
+        sh.range = Range{down < kSelSample ? sorted[(int)down] : 0u,
+                         up >= 0.0 ? sorted[(int)up] : 0xffffffffu, 0, 0};
     }
     __syncthreads();
 }
 
-__global__ void __launch_bounds__(kSelThreads)
+// The marking pass over the competitors [lo, hi): bits of `above` for the keys above
+// g.hi (not when it is null), and the positions of the keys in [g.lo, g.hi] listed as far
+// as the list has room; sh.above and sh.listed count them.  A thread compares four runs
+// of four positions with the range, as floats (the order of the keys, NaN apart), while the
+// next four are on their way; its warp makes room for all its finds with one addition.
+__device__ void mark_and_list(SelShared& sh, const float* score, int64_t lo, int64_t hi, Range g,
+                              uint32_t* above, int32_t* list_at) {
+    constexpr int kRuns = 4;
+    const int lane = threadIdx.x & 31;
+    const bool all = g.lo == 0u;  // then NaN too
+    const float floor = from_key(g.lo);
+    // past +inf no number lies above the range
+    const float ceil = g.hi < 0xff800000u ? from_key(g.hi) : INFINITY;
+    unsigned over = 0;
+    // at: position of v[0].x, the runs `step` positions apart; use: bit 4 u + j for each
+    // value that counts
+    auto take = [&](int64_t at, int step, const float4 (&v)[kRuns], unsigned use) {
+        unsigned in = 0, top = 0;
+#pragma unroll
+        for (int u = 0; u < kRuns; ++u) {
+            const float x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (x[j] >= floor) in |= 1u << (4 * u + j);
+                if (x[j] > ceil) top |= 1u << (4 * u + j);
+            }
+        }
+        if (all) in = 0xffffu;
+        in &= use & ~top;
+        top &= use;
+        over += __popc(top);
+        if (above != nullptr)
+            while (top) {
+                const int k = __ffs(top) - 1;
+                top &= top - 1;
+                const int p = (int)at + (k >> 2) * step + (k & 3);
+                atomicOr(&above[p >> 5], 1u << (p & 31));
+            }
+        if (!__any_sync(kAll, in)) return;
+        const int mine = __popc(in);
+        int inc = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(kAll, inc, d);
+            if (lane >= d) inc += o;
+        }
+        int base = 0;
+        if (lane == 31) base = atomicAdd(&sh.listed, inc);
+        base = __shfl_sync(kAll, base, 31) + inc - mine;
+        while (in) {
+            const int k = __ffs(in) - 1;
+            in &= in - 1;
+            if (base < kSelList) list_at[base] = (int)at + (k >> 2) * step + (k & 3);
+            ++base;
+        }
+        __syncwarp();
+    };
+    const int64_t skew = (int64_t)((reinterpret_cast<uintptr_t>(score + lo) & 15u) / 4);
+    int64_t head = lo + (skew ? 4 - skew : 0);
+    if (head > hi) head = hi;
+    const int64_t quads = (hi - head) / 4, tail = head + quads * 4;
+    const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (threadIdx.x < 32) {  // up to the first 16-byte boundary, and from the last on
+        const int64_t at = lane < 4 ? lo + lane : tail + lane - 4;
+        const bool on = lane < 4 ? at < head : lane < 8 && at < hi;
+        const float4 v[kRuns] = {make_float4(on ? score[at] : 0.f, 0.f, 0.f, 0.f), zero, zero, zero};
+        take(at, 0, v, on ? 1u : 0u);
+    }
+    const float4* s4 = reinterpret_cast<const float4*>(score + head);
+    auto load = [&](int64_t base, float4 (&x)[kRuns]) {
+#pragma unroll
+        for (int u = 0; u < kRuns; ++u) {
+            const int64_t i = base + u * kSelThreads + lane;
+            x[u] = i < quads ? __ldg(s4 + i) : zero;
+        }
+    };
+    float4 x[kRuns];
+    int64_t base = (int)threadIdx.x - lane;
+    load(base, x);
+    for (; base < quads; base += kRuns * kSelThreads) {
+        float4 next[kRuns];
+        load(base + kRuns * kSelThreads, next);
+        unsigned use = 0;
+#pragma unroll
+        for (int u = 0; u < kRuns; ++u)
+            if (base + u * kSelThreads + lane < quads) use |= 15u << (4 * u);
+        take(head + (base + lane) * 4, 4 * kSelThreads, x, use);
+#pragma unroll
+        for (int u = 0; u < kRuns; ++u) x[u] = next[u];
+    }
+    if (over) atomicAdd(&sh.above, (int)over);
+}
+
+__global__ void __launch_bounds__(kSelThreads, 2)
     evict_select_kernel(EvictArgs a, int64_t window, int32_t* positions, int32_t* lengths_out) {
     pdl_wait();
     extern __shared__ uint32_t sel_smem[];
@@ -229,7 +314,6 @@ __global__ void __launch_bounds__(kSelThreads)
     int32_t* list_at = (int32_t*)(sel_smem + kSelList);
     uint32_t* above_map = sel_smem + 2 * kSelList;  // a bit per position of a window
     uint32_t* tie_map = above_map + window / 32;
-    const int lane = threadIdx.x & 31;
     const int64_t r = blockIdx.x, b = r / a.H, h = r - b * a.H;
     const int64_t n = row_length(a, b);
     const float* score = a.score + b * a.score_b + h * a.score_h;
@@ -242,18 +326,18 @@ __global__ void __launch_bounds__(kSelThreads)
         return;
     }
     const int64_t lo = a.first, hi = n - a.last;  // the positions that compete
-    const int64_t need = a.budget - a.first - a.last;
+    const int need = (int)(a.budget - a.first - a.last);
     const bool one = n <= window;                 // the whole row fits the bit maps
     bool marked = false;                          // they are filled
     bool listed = false;                          // the list holds the range's keys
     if (need > 0) {
-        if (hi - lo <= kSelList) {
-            if (threadIdx.x == 0) sh.range = Range{0u, 0xffffffffu, 0, hi - lo};
+        if (hi - lo <= 2 * kSelSample) {
+            if (threadIdx.x == 0) sh.range = Range{0u, 0xffffffffu, 0, (int)(hi - lo)};
             __syncthreads();
         } else {
-            sample_range(sh, score, lo, hi, need);
+            sample_range(sh, list_key, score, lo, hi, need);
         }
-        bool known = hi - lo <= kSelList;  // the range's counts are exact
+        bool known = hi - lo <= 2 * kSelSample;  // the range's counts are exact
         // One pass marks and lists; when the range proves wrong or too full, histogram
         // passes narrow it until the list holds it, or until it is one key.
         for (;;) {
@@ -270,28 +354,10 @@ __global__ void __launch_bounds__(kSelThreads)
                     clear_words(tie_map, (n + 31) / 32);
                 }
                 __syncthreads();
-                unsigned over = 0;
-                each_key(score, lo, hi, [&](int64_t at, uint32_t key) {
-                    if (key < g.lo) return;
-                    if (key > g.hi) {
-                        ++over;
-                        if (one) atomicOr(&above_map[at >> 5], 1u << (at & 31));
-                        return;
-                    }
-                    const unsigned on = __activemask();
-                    const int lead = __ffs(on) - 1;
-                    int base = 0;
-                    if (lane == lead) base = atomicAdd(&sh.listed, __popc(on));
-                    base = __shfl_sync(on, base, lead) + __popc(on & ((1u << lane) - 1u));
-                    if (base < kSelList) {
-                        list_key[base] = key;
-                        list_at[base] = (int32_t)at;
-                    }
-                });
-                if (over) atomicAdd(&sh.above, (unsigned long long)over);
+                mark_and_list(sh, score, lo, hi, g, one ? above_map : nullptr, list_at);
                 __syncthreads();
                 if (threadIdx.x == 0) {
-                    sh.range.above = (int64_t)sh.above;
+                    sh.range.above = sh.above;
                     sh.range.inside = sh.listed;
                 }
                 __syncthreads();
@@ -302,13 +368,13 @@ __global__ void __launch_bounds__(kSelThreads)
                     if (listed) break;
                 } else {  // the sample missed
                     __syncthreads();
-                    if (threadIdx.x == 0) sh.range = Range{0u, 0xffffffffu, 0, hi - lo};
+                    if (threadIdx.x == 0) sh.range = Range{0u, 0xffffffffu, 0, (int)(hi - lo)};
                     __syncthreads();
                     known = true;
                 }
                 continue;
             }
-            for (int i = threadIdx.x; i < kSelBins; i += kSelThreads) sh.hist[i] = 0;
+            clear_words(sh.hist, kSelBins);
             __syncthreads();
             const int shift = range_shift(g.lo, g.hi);
             each_key(score, lo, hi, [&](int64_t, uint32_t key) {
@@ -318,15 +384,16 @@ __global__ void __launch_bounds__(kSelThreads)
         }
         if (listed) {
             const int m = (int)sh.range.inside;
+            for (int i = threadIdx.x; i < m; i += kSelThreads) list_key[i] = score_key(score[list_at[i]]);
             while (sh.range.lo != sh.range.hi) {
                 const Range g = sh.range;
                 __syncthreads();
-                for (int i = threadIdx.x; i < kSelBins; i += kSelThreads) sh.hist[i] = 0;
+                clear_words(sh.hist, kSelBins);
                 __syncthreads();
                 const int shift = range_shift(g.lo, g.hi);
                 for (int i = threadIdx.x; i < m; i += kSelThreads) {
                     const uint32_t key = list_key[i];
-                    if (key >= g.lo && key <= g.hi) count_bin(sh.hist, (int)((key - g.lo) >> shift));
+                    if (key >= g.lo && key <= g.hi) atomicAdd(&sh.hist[(key - g.lo) >> shift], 1u);
                 }
                 narrow_range(sh, need);
             }
@@ -345,8 +412,12 @@ __global__ void __launch_bounds__(kSelThreads)
     __syncthreads();
     const uint32_t cut = need > 0 ? sh.range.lo : 0xffffffffu;
     const int64_t ties = need > 0 ? need - sh.range.above : 0;  // competitors at the cut that stay
-    // out of the bit maps, a window of positions at a time
-    int64_t out = 0, tied = 0;
+    // the first and the last stay whatever their scores
+    for (int64_t i = threadIdx.x; i < a.first; i += kSelThreads) pos[i] = (int32_t)i;
+    for (int64_t i = threadIdx.x; i < a.last; i += kSelThreads)
+        pos[a.budget - a.last + i] = (int32_t)(hi + i);
+    // the competitors out of the bit maps, a window of positions at a time
+    int64_t out = a.first, tied = 0;
     for (int64_t w0 = 0; w0 < n; w0 += window) {
         const int64_t w1 = w0 + window < n ? w0 + window : n;
         const int words = (int)((w1 - w0 + 31) / 32);
@@ -364,39 +435,34 @@ __global__ void __launch_bounds__(kSelThreads)
                          });
             __syncthreads();
         }
-        for (int base = 0; base < words; base += kSelThreads) {
-            const int i = base + threadIdx.x;
-            uint32_t A = 0, T = 0;
-            if (i < words) {
-                A = above_map[i];
-                T = tie_map[i];
-                // the first and the last stay whatever their scores
-                const int64_t p0 = w0 + (int64_t)i * 32;
-                const int64_t c = lo - p0, d = hi - p0;
-                if (c > 0) A |= c >= 32 ? kAll : (1u << c) - 1u;
-                if (d < 32) A |= d <= 0 ? kAll : kAll << d;
-                if (n - p0 < 32) A &= (1u << (n - p0)) - 1u;
-            }
-            int2 tot;
-            const int2 at = block_prefix(make_int2(__popc(A), __popc(T)), &tot, sh.sums);
-            // kept before this word: its A bits and the ties among the first `ties`
-            const int64_t t0 = tied + at.y;
-            const int64_t was = tied < ties ? tied : ties;
-            int64_t o = out + at.x + ((t0 < ties ? t0 : ties) - was);
-            int64_t left = ties - t0;
-            uint32_t bits = A | T;
+        // each thread owns a run of words: its kept competitors come after those of lower
+        // threads; of the ties only the first `ties` of the row count
+        const int per = (words + kSelThreads - 1) / kSelThreads;
+        const int i0 = threadIdx.x * per, i1 = i0 + per < words ? i0 + per : words;
+        int2 mine = make_int2(0, 0);
+        for (int i = i0; i < i1; ++i) {
+            mine.x += __popc(above_map[i]);
+            mine.y += __popc(tie_map[i]);
+        }
+        int2 tot;
+        const int2 at = block_prefix(mine, &tot, sh.sums);
+        const int64_t was = tied < ties ? tied : ties;
+        const int64_t t0 = tied + at.y;
+        int64_t o = out + at.x + ((t0 < ties ? t0 : ties) - was);
+        int64_t left = ties - t0;
+        for (int i = i0; i < i1; ++i) {
+            const uint32_t T = tie_map[i];
+            uint32_t bits = above_map[i] | T;
             while (bits) {
                 const int k = __ffs(bits) - 1;
                 bits &= bits - 1;
-                if ((T >> k) & 1u) {
-                    if (left-- <= 0) continue;
-                }
+                if (((T >> k) & 1u) && left-- <= 0) continue;
                 pos[o++] = (int32_t)(w0 + (int64_t)i * 32 + k);
             }
-            const int64_t t2 = tied + tot.y;
-            out += tot.x + ((t2 < ties ? t2 : ties) - was);
-            tied = t2;
         }
+        const int64_t t2 = tied + tot.y;
+        out += tot.x + ((t2 < ties ? t2 : ties) - was);
+        tied = t2;
     }
 }
 
