@@ -6,6 +6,10 @@ import torch
 
 from . import LapSumError
 
+# the calls behind torch.cuda.current_device and current_stream, without building a Stream
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
@@ -13,32 +17,36 @@ def launch(fn, device, *args):
     """Calls the library function with the current stream of ``device`` as its last
     argument, on that device whatever the current one is; raises on an error."""
     index = device.index
-    if index == torch.cuda.current_device():
-        code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if index == _current_device():
+        code = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            code = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+            code = fn(*args, _raw_stream(index))
     if code != 0:
         raise LapSumError(code, fn.__name__)
 
 
 def need(x, name: str, dtypes, dim: int, device=None):
     """x must be a CUDA tensor of one of ``dtypes`` with ``dim`` dimensions, on ``device``."""
+    if isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in dtypes and x.dim() == dim and \
+            (device is None or x.device == device):
+        return
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype not in dtypes:
         kinds = ", ".join(str(d).replace("torch.", "") for d in dtypes)
         raise TypeError(f"{name} must be a CUDA tensor of {kinds}")
     if x.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions")
-    if device is not None and x.device != device:
-        raise ValueError(f"{name} is on {x.device}, not on {device}")
+    raise ValueError(f"{name} is on {x.device}, not on {device}")
 
 
 def extent(x: torch.Tensor):
     """First and one past the last byte that x's elements span."""
-    if x.numel() == 0:
-        return x.data_ptr(), x.data_ptr()
-    span = sum((n - 1) * s for n, s in zip(x.shape, x.stride())) + 1
-    return x.data_ptr(), x.data_ptr() + span * x.element_size()
+    start, span = x.data_ptr(), 1
+    for n, s in zip(x.shape, x.stride()):
+        if n == 0:
+            return start, start
+        span += (n - 1) * s
+    return start, start + span * x.element_size()
 
 
 def overlap(x: torch.Tensor, y: torch.Tensor) -> bool:
@@ -48,6 +56,8 @@ def overlap(x: torch.Tensor, y: torch.Tensor) -> bool:
 
 def distinct(x: torch.Tensor) -> bool:
     """Whether no two of x's elements share memory (strides nest without overlap)."""
+    if x.is_contiguous():
+        return True
     need_stride = 1
     for s, n in sorted((s, n) for n, s in zip(x.shape, x.stride()) if n > 1):
         if s < need_stride:

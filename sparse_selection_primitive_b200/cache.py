@@ -17,20 +17,25 @@ from . import _lib
 from ._launch import DTYPES, distinct, extent, launch, need, overlap
 
 _HALF = (torch.bfloat16, torch.float16)
+_F32, _I32 = (torch.float32,), (torch.int32,)
+_Strides13, _Strides16 = ctypes.c_int64 * 13, ctypes.c_int64 * 16
 
 
 def _check_caches(k, v, score, lengths, dtypes):
     need(k, "k", dtypes, 4)
-    need(v, "v", (k.dtype,), 4, k.device)
-    need(score, "score", (torch.float32,), 3, k.device)
-    need(lengths, "lengths", (torch.int32,), 1, k.device)
-    if v.shape != k.shape or score.shape != k.shape[:3] or lengths.shape[0] != k.shape[0]:
+    dev, shape = k.device, k.shape
+    need(v, "v", (k.dtype,), 4, dev)
+    need(score, "score", _F32, 3, dev)
+    need(lengths, "lengths", _I32, 1, dev)
+    if v.shape != shape or score.shape != shape[:3] or lengths.shape[0] != shape[0]:
         raise ValueError("k and v must be (B, H, N, D), score (B, H, N) and lengths (B)")
-    for x, name in ((k, "k"), (v, "v"), (score, "score")):
-        if x.shape[-1] > 1 and x.stride(-1) != 1:
+    strides = k.stride(), v.stride(), score.stride()
+    for s, n, name in zip(strides, (shape[3], shape[3], shape[2]), ("k", "v", "score")):
+        if s[-1] != 1 and n > 1:
             raise ValueError(f"{name} must be consecutive in its last dimension")
     if not lengths.is_contiguous():
         raise ValueError("lengths must be contiguous")
+    return strides
 
 
 def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths: torch.Tensor,
@@ -45,21 +50,23 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
     A token i sees the keys before lengths - Sq + i + 1; one that sees none gets 0.
     ``scale`` is D ** -0.5 by default.  D is a multiple of 16 up to 256; the tensors may
     be strided views whose rows start on 16 bytes.  No gradient."""
-    _check_caches(k, v, score, lengths, _HALF)
+    ks, vs, ss = _check_caches(k, v, score, lengths, _HALF)
     need(q, "q", (k.dtype,), 4, k.device)
     B, Sq, Hq, D = q.shape
-    Hkv, N = k.shape[1], k.shape[2]
+    _, Hkv, N, _ = k.shape
+    qs = q.stride()
     if B != k.shape[0] or D != k.shape[3] or Hkv < 1 or Hq % Hkv != 0:
         raise ValueError("q must be (B, Sq, Hq, D) with Hq a multiple of the caches' heads")
-    if D > 1 and q.stride(3) != 1:
+    if D > 1 and qs[3] != 1:
         raise ValueError("q must be consecutive in its last dimension")
     if score_out is None:
-        score_out = score
+        score_out, outs = score, ss
     else:
-        need(score_out, "score_out", (torch.float32,), 3, k.device)
-        if score_out.shape != score.shape or N > 1 and score_out.stride(2) != 1:
+        need(score_out, "score_out", _F32, 3, k.device)
+        outs = score_out.stride()
+        if score_out.shape != score.shape or N > 1 and outs[2] != 1:
             raise ValueError("score_out must have score's shape, consecutive in its last dimension")
-        same = score_out.data_ptr() == score.data_ptr() and score_out.stride() == score.stride()
+        same = outs == ss and score_out.data_ptr() == score.data_ptr()
         if not same and overlap(score, score_out):
             raise ValueError("score_out must be score itself or not overlap it")
     if not distinct(score_out):
@@ -72,14 +79,14 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
             raise ValueError("out must be contiguous and have q's shape")
         if any(overlap(out, x) for x in (q, k, v, score, score_out)):
             raise ValueError("out must not overlap the inputs")
-    if out.numel() == 0:
+    if B * Sq * Hq * D == 0:
         if score_out is not score and B * Hkv * N > 0:
             raise ValueError("nothing to attend with: Sq is 0")
         return out
     if N == 0:
         return out.zero_()
-    strides = (ctypes.c_int64 * 13)(q.stride(0), q.stride(2), q.stride(1), *k.stride()[:3],
-                                    *v.stride()[:3], *score.stride()[:2], *score_out.stride()[:2])
+    strides = _Strides13(qs[0], qs[2], qs[1], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], ss[0],
+                         ss[1], outs[0], outs[1])
     lib = _lib()
     nbytes = lib.lapsum_attend_workspace_bytes(B, Sq, Hq, Hkv, N, D)
     ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
@@ -110,7 +117,7 @@ def evict(k: torch.Tensor, v: torch.Tensor, score: torch.Tensor, lengths: torch.
     ``out`` may hold the caches and scores to fill, (k, v, score) with at least
     ``budget`` rows; rows from ``budget`` on are left as they were.  Rows that no key
     fills (fewer than ``budget`` in the cache) are 0 and their positions -1."""
-    _check_caches(k, v, score, lengths, DTYPES)
+    ks, vs, ss = _check_caches(k, v, score, lengths, DTYPES)
     B, H, N, D = k.shape
     budget, first, last = int(budget), int(first), int(last)
     if budget < 1 or first < 0 or last < 0 or first + last > budget:
@@ -140,8 +147,8 @@ def evict(k: torch.Tensor, v: torch.Tensor, score: torch.Tensor, lengths: torch.
             raise ValueError("the caches must hold at least one row of one element")
         left.copy_(lengths.clamp(0, min(N, budget)))
         return result
-    strides = (ctypes.c_int64 * 16)(*k.stride()[:3], *v.stride()[:3], *score.stride()[:2],
-                                    *ko.stride()[:3], *vo.stride()[:3], *so.stride()[:2])
+    strides = _Strides16(*ks[:3], *vs[:3], *ss[:2], *ko.stride()[:3], *vo.stride()[:3],
+                         *so.stride()[:2])
     launch(_lib().lapsum_evict, k.device, k.data_ptr(), v.data_ptr(), DTYPES[k.dtype],
            score.data_ptr(), lengths.data_ptr(), strides, B, H, N, D, budget, first, last,
            ko.data_ptr(), vo.data_ptr(), so.data_ptr(), positions.data_ptr(), left.data_ptr())

@@ -56,36 +56,48 @@ def route_backward(logits: torch.Tensor, weights: torch.Tensor, experts: torch.T
         raise ValueError("weights, experts and dweights must be (rows of logits) x k")
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
-    logits, weights, experts = _rows(logits), weights.contiguous(), experts.contiguous()
-    dweights = dweights.contiguous()
+    return _route_grad(_rows(logits), weights.contiguous(), experts.contiguous(),
+                       dweights.contiguous(), SCORES[score], bool(renormalize), float(scale))
+
+
+def _once(backward):
+    """once_differentiable, without its cost in a plain backward pass (no create_graph)."""
+    checked = once_differentiable(backward)
+
+    def run(ctx, *grads):
+        return (checked if torch.is_grad_enabled() else backward)(ctx, *grads)
+    return staticmethod(run)
+
+
+def _route_grad(logits, weights, experts, dweights, score, renormalize, scale):
     T, E = logits.shape
     out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
     if T > 0:
         launch(_lib().lapsum_route_backward, logits.device, logits.data_ptr(),
-               DTYPES[logits.dtype], _ld(logits), T, E, experts.shape[1], SCORES[score],
-               bool(renormalize), float(scale), weights.data_ptr(), experts.data_ptr(),
-               dweights.data_ptr(), out.data_ptr(), E)
+               DTYPES[logits.dtype], _ld(logits), T, E, experts.shape[1], score, renormalize,
+               scale, weights.data_ptr(), experts.data_ptr(), dweights.data_ptr(), out.data_ptr(),
+               E)
     return out
 
 
 class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, k, score, bias, groups, top_groups, group_top, renormalize, scale):
-        weights, experts = _route(logits.detach(), k, SCORES[score], bias, groups, top_groups,
-                                  group_top, renormalize, scale)
+        weights, experts = _route(logits, k, score, bias, groups, top_groups, group_top,
+                                  renormalize, scale)
         ctx.save_for_backward(logits, weights, experts)
         ctx.how = (score, renormalize, scale)
         ctx.mark_non_differentiable(experts)
         ctx.set_materialize_grads(False)
         return weights, experts
 
-    @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, dweights, _):
         if dweights is None:
             return (None,) * 9
         logits, weights, experts = ctx.saved_tensors
-        return (route_backward(logits, weights, experts, dweights, *ctx.how),) + (None,) * 8
+        return (_route_grad(logits, weights, experts, dweights.contiguous(), *ctx.how),
+                None, None, None, None, None, None, None, None)
 
 
 def route_experts(logits: torch.Tensor, k: int, *, score: str = "softmax", bias=None,
@@ -115,11 +127,8 @@ def route_experts(logits: torch.Tensor, k: int, *, score: str = "softmax", bias=
         bias = bias.detach().contiguous()
     logits = _rows(logits)
     renormalize, scale = bool(renormalize), float(scale)
-    if logits.requires_grad and torch.is_grad_enabled():
-        return _Route.apply(logits, k, score, bias, groups, top_groups, group_top, renormalize,
-                            scale)
-    return _route(logits, k, SCORES[score], bias, groups, top_groups, group_top, renormalize,
-                  scale)
+    run = _Route.apply if logits.requires_grad and torch.is_grad_enabled() else _route
+    return run(logits, k, SCORES[score], bias, groups, top_groups, group_top, renormalize, scale)
 
 
 class ExpertPlan(NamedTuple):
@@ -189,10 +198,9 @@ class _Gather(torch.autograd.Function):
     def forward(ctx, x, offsets, slots, order):
         plan = ExpertPlan(offsets, slots, order)
         ctx.save_for_backward(offsets, slots)
-        return _gather(x.detach(), plan)
+        return _gather(x, plan)
 
-    @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, dxs):
         offsets, slots = ctx.saved_tensors
         return _combine(dxs.contiguous(), None, ExpertPlan(offsets, slots, None)), None, None, None
@@ -215,10 +223,9 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, offsets, slots):
         ctx.save_for_backward(y, weights, offsets, slots)
-        return _combine(y.detach(), weights.detach(), ExpertPlan(offsets, slots, None))
+        return _combine(y, weights, ExpertPlan(offsets, slots, None))
 
-    @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, dout):
         y, weights, offsets, slots = ctx.saved_tensors
         plan = ExpertPlan(offsets, slots, None)
