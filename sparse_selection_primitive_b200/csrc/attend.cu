@@ -29,7 +29,7 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kTile = 128;          // keys per tile: the M of S^T
-constexpr int kSplitThreads = 192;  // warp 0 loads, warp 1 multiplies, warps 2-5 do the softmax
+constexpr int kKeepRows = 16;       // logits of more rows a key are formed again, not kept
 constexpr int kMaxStages = 6;
 constexpr int kMaxTiles = 32;
 constexpr int kJoinThreads = 256;
@@ -51,8 +51,16 @@ struct AttendPlan {
     int splits;     // runs of key tiles per row tile
     int tiles;      // most key tiles per run
     int stages, cols, smem;
+    int keep;       // the logits are kept for the scores
     int64_t RP;     // rows of logits per key, padded
-    size_t off_part, off_logits, bytes;
+    size_t off_lse, off_part, off_logits, bytes;
+};
+
+// The score pass over keys whose logits were not kept.
+constexpr int kScoreRows = 128, kScoreThreads = 64 + 256;
+struct ScorePlan {
+    int blocks;  // blocks of a key/value head
+    int stages, smem;
 };
 
 __device__ __forceinline__ int64_t cache_length(const AttendArgs& a, int64_t b) {
@@ -94,7 +102,34 @@ __device__ __forceinline__ void join_lanes(float (&v)[N], int lane, F f) {
     }
 }
 
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void softmax_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
+
+// A tile of RT rows of q from row0 on into shared memory, zero beyond the rows and beyond
+// D, in the layout that TMA gives the keys (128-byte rows, 16-byte chunks exchanged by row).
+template <class T, int RT>
+__device__ __forceinline__ void load_rows(const AttendArgs& a, const T* q, int b, int h,
+                                          int64_t row0, int rows, uint32_t to, int thread,
+                                          int threads) {
+    const uint32_t chunks = (a.D + 63) / 64 * 8;
+#pragma unroll 4
+    for (uint32_t i = thread; i < RT * chunks; i += threads) {
+        const uint32_t r = i / chunks, c = i - r * chunks;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < (uint32_t)rows && c * 8 < (uint32_t)a.D) {
+            const uint32_t row = (uint32_t)row0 + r, tok = row / (uint32_t)a.G,
+                           g = row - tok * (uint32_t)a.G;
+            x = *reinterpret_cast<const uint4*>(q + b * a.qb + tok * a.qr +
+                                                ((int64_t)h * a.G + g) * a.qh + c * 8);
+        }
+        const uint32_t at = to + (c >> 3) * (RT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y),
+                     "r"(x.z), "r"(x.w)
+                     : "memory");
+    }
+}
 
 template <class T>
 struct Pair;  // two 16-bit values in a word
@@ -116,9 +151,11 @@ struct Pair<__half> {
 };
 
 // One run of key tiles for one tile of rows.  Writes the run's row maxima and sums
-// (stats), its unnormalised outputs (part) and the logits, all in fp32.
-template <class T, int RT>
-__global__ void __launch_bounds__(kSplitThreads)
+// (stats), its unnormalised outputs (part) and, where they are kept, the logits, all in
+// fp32.  Warp 0 loads, warp 1 multiplies, and 4 CW warps do the softmax: a warp can read
+// one quarter of the lanes of tensor memory, and CW warps share the rows of a quarter.
+template <class T, int RT, int CW>
+__global__ void __launch_bounds__(64 + 128 * CW, 1)
     attend_split_kernel(AttendArgs a, AttendPlan p, const T* q,
                         const __grid_constant__ CUtensorMap k_map,
                         const __grid_constant__ CUtensorMap v_map, float2* stats, float* part,
@@ -127,6 +164,8 @@ __global__ void __launch_bounds__(kSplitThreads)
     __shared__ uint64_t bars[2 * kMaxStages + kMaxTiles + 2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_failed;
+    constexpr int RC = RT / CW;  // rows of a softmax warp
+    constexpr int kSoftmax = 128 * CW;
     __shared__ float red[4][RT];
     __shared__ alignas(16) float s_max[RT];
     __shared__ alignas(16) int s_lim[RT];  // keys that each row sees, from the run's first
@@ -168,7 +207,7 @@ __global__ void __launch_bounds__(kSplitThreads)
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < tiles; ++i) mbar_init(s_done + 8 * i, 1);
-        mbar_init(p_full, 128);
+        mbar_init(p_full, kSoftmax);
         mbar_init(p_empty, 1);
         fence_barrier_init();
         s_failed = 0;
@@ -179,20 +218,7 @@ __global__ void __launch_bounds__(kSplitThreads)
         s_lim[threadIdx.x] = (int)(threadIdx.x < rows && lim < tiles * kTile ? lim : tiles * kTile);
     }
     if (warp == 1) tmem_alloc(smem_addr(&s_tmem), p.cols);
-    // the row tile, zero beyond the rows and beyond D, in the layout TMA gives the keys
-    for (int i = threadIdx.x; i < RT * subs * 8; i += kSplitThreads) {
-        const int r = i / (subs * 8), c = i % (subs * 8);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < rows && c * 8 < a.D) {
-            const int64_t row = row0 + r, tok = row / a.G, g = row - tok * a.G;
-            x = *reinterpret_cast<const uint4*>(q + b * a.qb + tok * a.qr +
-                                                ((int64_t)h * a.G + g) * a.qh + c * 8);
-        }
-        const uint32_t at = q_at + (c >> 3) * (RT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y),
-                     "r"(x.z), "r"(x.w)
-                     : "memory");
-    }
+    load_rows<T, RT>(a, q, b, h, row0, rows, q_at, threadIdx.x, 64 + kSoftmax);
     fence_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -260,11 +286,12 @@ __global__ void __launch_bounds__(kSplitThreads)
     } else {
         const int quarter = warp & 3;                  // the lanes of tensor memory it may read
         const int key = quarter * 32 + lane;           // of a tile
-        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const int c0 = (warp - 2) / 4 * RC;            // its first row
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
         const int tid = threadIdx.x - 64;
-        float top[RT];
+        float top[RC];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) top[r] = -INFINITY;
+        for (int r = 0; r < RC; ++r) top[r] = -INFINITY;
         // phase 1: logits, their maxima
         for (int t = 0; t < tiles && ok; ++t) {
             ok = mbar_wait(s_done + 8 * t, 0);
@@ -273,53 +300,53 @@ __global__ void __launch_bounds__(kSplitThreads)
                 break;
             }
             tc_fence_after();
-            float x[RT];
-            tmem_ld<RT>(lanes + t * RT, x);
+            float x[RC];
+            tmem_ld<RC>(lanes + t * RT, x);
             const int64_t j = (first + t) * kTile + key;
             const bool whole = (t + 1) * kTile <= s_lim[0];  // the first row sees the fewest
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
+            for (int r = 0; r < RC; ++r) {
                 x[r] *= a.scale_log2;
-                if (!whole && t * kTile + key >= s_lim[r]) x[r] = -INFINITY;
+                if (!whole && t * kTile + key >= s_lim[c0 + r]) x[r] = -INFINITY;
                 top[r] = fmaxf(top[r], x[r]);
             }
-            if (j < n) {
-                float* to = logits + (bh * a.N + j) * p.RP + row0;
+            if (p.keep && j < n) {
+                float* to = logits + (bh * a.N + j) * p.RP + row0 + c0;
 #pragma unroll
-                for (int r = 0; r < RT; r += 4)
-                    if (row0 + r < p.RP)
+                for (int r = 0; r < RC; r += 4)
+                    if (row0 + c0 + r < p.RP)
                         *reinterpret_cast<float4*>(to + r) =
                             make_float4(x[r], x[r + 1], x[r + 2], x[r + 3]);
             }
         }
-        join_lanes<RT>(top, lane, [](float u, float w) { return fmaxf(u, w); });
-        constexpr int kOwn = RT > 32 ? RT / 32 : 1;
-        const int at = joined_at<RT>(lane);
+        join_lanes<RC>(top, lane, [](float u, float w) { return fmaxf(u, w); });
+        constexpr int kOwn = RC > 32 ? RC / 32 : 1;
+        const int at = joined_at<RC>(lane);
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) red[quarter][at + i] = top[i];
-        softmax_sync();
+        for (int i = 0; i < kOwn; ++i) red[quarter][c0 + at + i] = top[i];
+        softmax_sync<kSoftmax>();
         if (tid < RT) {
             const float m = fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid]));
             s_max[tid] = m == -INFINITY ? 0.f : m;
         }
-        softmax_sync();
+        softmax_sync<kSoftmax>();
         // phase 2: weights relative to the run's maximum
-        float sum[RT];
+        float sum[RC];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) sum[r] = 0.f;
+        for (int r = 0; r < RC; ++r) sum[r] = 0.f;
         for (int t = 0; t < tiles && ok; ++t) {
-            float x[RT];
-            tmem_ld<RT>(lanes + t * RT, x);
+            float x[RC];
+            tmem_ld<RC>(lanes + t * RT, x);
             const int64_t j0 = (first + t) * kTile, j = j0 + key;
             const bool whole = (t + 1) * kTile <= s_lim[0];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                x[r] = ex2_ftz(__fmul_rn(x[r], a.scale_log2) - s_max[r]);
-                if (!whole && t * kTile + key >= s_lim[r]) x[r] = 0.f;
+            for (int r = 0; r < RC; ++r) {
+                x[r] = ex2_ftz(__fmul_rn(x[r], a.scale_log2) - s_max[c0 + r]);
+                if (!whole && t * kTile + key >= s_lim[c0 + r]) x[r] = 0.f;
                 sum[r] += x[r];
             }
             if (t > 0) ok = mbar_wait(p_empty, (t - 1) & 1);
-            if (j0 + kTile > n) {
+            if (j0 + kTile > n && c0 == 0) {
                 // value rows behind the cache's end may hold anything: 0 x NaN is NaN
                 const int item = tiles + t, s = item % p.stages;
                 ok = ok && mbar_wait(full + 8 * s, (item / p.stages) & 1);
@@ -336,7 +363,7 @@ __global__ void __launch_bounds__(kSplitThreads)
                 break;
             }
 #pragma unroll
-            for (int r = 0; r < RT; r += 8) {
+            for (int r = 0; r < RC; r += 8) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -345,7 +372,7 @@ __global__ void __launch_bounds__(kSplitThreads)
                     const T* parts = reinterpret_cast<const T*>(&hi[i]);
                     lo[i] = Pair<T>::pack(u - widen(parts[0]), w - widen(parts[1]));
                 }
-                const uint32_t to = p_at + (r >> 3) * 2048 + key * 16;
+                const uint32_t to = p_at + ((c0 + r) >> 3) * 2048 + key * 16;
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]),
                              "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
                              : "memory");
@@ -357,12 +384,12 @@ __global__ void __launch_bounds__(kSplitThreads)
             tc_fence_before();
             mbar_arrive(p_full);
         }
-        join_lanes<RT>(sum, lane, [](float u, float w) { return u + w; });
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) red[quarter][at + i] = sum[i];
+        join_lanes<RC>(sum, lane, [](float u, float w) { return u + w; });
         if (ok) ok = mbar_wait(p_empty, (tiles - 1) & 1);
         if (!ok) s_failed = 1;
-        softmax_sync();
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) red[quarter][c0 + at + i] = sum[i];
+        softmax_sync<kSoftmax>();
         tc_fence_after();
         if (tid < rows) {
             const float l = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
@@ -373,14 +400,14 @@ __global__ void __launch_bounds__(kSplitThreads)
         }
         if (!s_failed)
             for (int m = 0; m * 128 < a.D; ++m) {
-                float o[RT];
-                tmem_ld<RT>(lanes + tiles * RT + m * RT, o);
+                float o[RC];
+                tmem_ld<RC>(lanes + tiles * RT + m * RT, o);
                 const int d = m * 128 + key;
                 if (d < a.D) {
-                    float* to = part + ((bh * p.splits + split) * a.R + row0) * a.D + d;
+                    float* to = part + ((bh * p.splits + split) * a.R + row0 + c0) * a.D + d;
 #pragma unroll
-                    for (int r = 0; r < RT; ++r)
-                        if (r < rows) to[(int64_t)r * a.D] = o[r];
+                    for (int r = 0; r < RC; ++r)
+                        if (c0 + r < rows) to[(int64_t)r * a.D] = o[r];
                 }
             }
         tc_fence_before();
@@ -393,67 +420,63 @@ __global__ void __launch_bounds__(kSplitThreads)
     }
 }
 
-// log2 of the sum of 2^x over all of a row's runs; +inf for a row that saw nothing.
-__device__ __forceinline__ float row_lse(const float2* stats, int splits, int64_t R) {
-    float m = -INFINITY;
+// log2 of the sum of 2^x over all of a row's runs, by one warp; +inf for a row that saw
+// nothing.
+__device__ __forceinline__ float row_lse(const float2* stats, int splits, int64_t R, int lane) {
+    float m = -INFINITY, l = 0.f;
     bool bad = false;
-    for (int s = 0; s < splits; ++s) {
+    for (int s = lane; s < splits; s += 32) {
         const float2 x = stats[s * R];
         bad |= isnan(x.x) || isnan(x.y);
-        m = fmaxf(m, x.x);
+        if (!(x.y > 0.f)) continue;
+        const float to = fmaxf(m, x.x);
+        l = l * ex2_ftz(m - to) + x.y * ex2_ftz(x.x - to);
+        m = to;
     }
-    if (bad) return NAN;
-    float l = 0.f;
-    for (int s = 0; s < splits; ++s) {
-        const float2 x = stats[s * R];
-        if (x.y > 0.f) l += x.y * ex2_ftz(x.x - m);
-    }
-    return l > 0.f ? m + log2f(l) : INFINITY;
+    if (__any_sync(kAll, bad)) return NAN;
+    float all = m;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) all = fmaxf(all, __shfl_xor_sync(kAll, all, d));
+    l = m > -INFINITY ? l * ex2_ftz(m - all) : 0.f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(kAll, l, d);
+    return l > 0.f ? all + log2f(l) : INFINITY;
 }
 
-// Joins the runs.  The first blocks turn logits into scores, one thread a key; the
-// others join the outputs, one warp a row.
+// Joins the runs.  The first blocks turn kept logits into scores, one thread a key; the
+// others join the outputs, one warp a row, and leave each row's log of the sum.
 template <class T>
 __global__ void __launch_bounds__(kJoinThreads)
     attend_join_kernel(AttendArgs a, AttendPlan p, int64_t score_blocks, int key_blocks,
                        const float2* stats, const float* part, const float* logits,
-                       const float* score_in, float* score_out, T* out) {
+                       const float* score_in, float* score_out, float* row_logs, T* out) {
     pdl_wait();
-    constexpr int kRows = 1024;
-    __shared__ alignas(16) float lse[kRows];
+    __shared__ alignas(16) float lse[kKeepRows];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x < score_blocks) {
         const int64_t bh = blockIdx.x / key_blocks, b = bh / a.Hkv, h = bh - b * a.Hkv;
         const int64_t n = cache_length(a, b);
         const int64_t j0 = (int64_t)(blockIdx.x % key_blocks) * kJoinThreads, j = j0 + threadIdx.x;
         if (j0 >= n) return;
+        for (int r = warp; r < p.RP; r += kJoinThreads / 32) {
+            const float v = r < a.R ? row_lse(stats + bh * p.splits * a.R + r, p.splits, a.R, lane)
+                                    : INFINITY;
+            if (lane == 0) lse[r] = v;
+        }
+        __syncthreads();
+        if (j >= n) return;
         // rows from this one on see key j
         const int64_t past = j - (n - a.Sq);
-        const int64_t from = past > 0 ? past * a.G : 0;
+        const float* x = logits + (bh * a.N + j) * p.RP;
         float s = 0.f;
-        for (int64_t base = 0; base < p.RP; base += kRows) {
-            const int cnt = (int)(p.RP - base < kRows ? p.RP - base : kRows);
-            __syncthreads();
-            for (int r = threadIdx.x; r < cnt; r += kJoinThreads)
-                lse[r] = base + r < a.R
-                             ? row_lse(stats + bh * p.splits * a.R + base + r, p.splits, a.R)
-                             : INFINITY;
-            __syncthreads();
-            if (j < n) {
-                const float* x = logits + (bh * a.N + j) * p.RP + base;
-                int r = (int)(from > base ? (from - base < cnt ? from - base : cnt) : 0) & ~3;
-                for (; r < cnt; r += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(x + r);
-                    const float4 w = *reinterpret_cast<const float4*>(lse + r);
-                    s += ex2_ftz(v.x - w.x) + ex2_ftz(v.y - w.y);
-                    s += ex2_ftz(v.z - w.z) + ex2_ftz(v.w - w.w);
-                }
-            }
+        for (int r = (int)(past > 0 ? past * a.G : 0) & ~3; r < p.RP; r += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(x + r);
+            const float4 w = *reinterpret_cast<const float4*>(lse + r);
+            s += ex2_ftz(v.x - w.x) + ex2_ftz(v.y - w.y);
+            s += ex2_ftz(v.z - w.z) + ex2_ftz(v.w - w.w);
         }
-        if (j < n) {
-            const float old = score_in != nullptr ? score_in[b * a.sib + h * a.sih + j] : 0.f;
-            score_out[b * a.sob + h * a.soh + j] = old + s;
-        }
+        const float old = score_in != nullptr ? score_in[b * a.sib + h * a.sih + j] : 0.f;
+        score_out[b * a.sob + h * a.soh + j] = old + s;
         return;
     }
     const int64_t row = (blockIdx.x - score_blocks) * (kJoinThreads / 32) + warp;
@@ -461,31 +484,193 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int64_t bh = row / a.R, r = row - bh * a.R, b = bh / a.Hkv, h = bh - b * a.Hkv;
     const int64_t tok = r / a.G, g = r - tok * a.G;
     const float2* st = stats + bh * p.splits * a.R + r;
-    const float top = row_lse(st, p.splits, a.R);  // the same on all lanes
+    const float top = row_lse(st, p.splits, a.R, lane);
+    if (lane == 0 && !p.keep) row_logs[row] = top;
     T* to = out + ((b * a.Sq + tok) * a.Hkv * a.G + h * a.G + g) * a.D;
-    for (int d = lane * 4; d < a.D; d += 128) {
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (isnan(top)) {
-            acc = make_float4(NAN, NAN, NAN, NAN);
-        } else {
-            for (int s = 0; s < p.splits; ++s) {
-                const float2 x = st[s * a.R];
-                if (!(x.y > 0.f)) continue;
-                const float w = ex2_ftz(x.x - top);
-                const float4 o = *reinterpret_cast<const float4*>(
-                    part + ((bh * p.splits + s) * a.R + r) * a.D + d);
-                acc.x = fmaf(w, o.x, acc.x);
-                acc.y = fmaf(w, o.y, acc.y);
-                acc.z = fmaf(w, o.z, acc.z);
-                acc.w = fmaf(w, o.w, acc.w);
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int d0 = 0; d0 < a.D; d0 += 128) {
+        const int d = d0 + lane * 4;
+        float4 acc = none;
+        for (int s0 = 0; s0 < p.splits; s0 += 32) {
+            const float2 x = s0 + lane < p.splits ? st[(s0 + lane) * a.R] : make_float2(0.f, 0.f);
+            // a run in which the row saw nothing has written no outputs: weight 0, not read
+            const float w = x.y > 0.f ? ex2_ftz(x.x - top) : 0.f;
+            const int cnt = p.splits - s0 < 32 ? p.splits - s0 : 32;
+#pragma unroll 8
+            for (int s = 0; s < cnt; ++s) {
+                const float ws = __shfl_sync(kAll, w, s);
+                const float4 o = ws > 0.f && d < a.D
+                                     ? *reinterpret_cast<const float4*>(
+                                           part + ((bh * p.splits + s0 + s) * a.R + r) * a.D + d)
+                                     : none;
+                acc.x = fmaf(ws, o.x, acc.x);
+                acc.y = fmaf(ws, o.y, acc.y);
+                acc.z = fmaf(ws, o.z, acc.z);
+                acc.w = fmaf(ws, o.w, acc.w);
             }
         }
-        Pack<T, 4> o;
-        o.v[0] = narrow<T>(acc.x);
-        o.v[1] = narrow<T>(acc.y);
-        o.v[2] = narrow<T>(acc.z);
-        o.v[3] = narrow<T>(acc.w);
-        *reinterpret_cast<Pack<T, 4>*>(to + d) = o;
+        if (isnan(top)) acc = make_float4(NAN, NAN, NAN, NAN);
+        if (d < a.D) {
+            Pack<T, 4> o;
+            o.v[0] = narrow<T>(acc.x);
+            o.v[1] = narrow<T>(acc.y);
+            o.v[2] = narrow<T>(acc.z);
+            o.v[3] = narrow<T>(acc.w);
+            *reinterpret_cast<Pack<T, 4>*>(to + d) = o;
+        }
+    }
+}
+
+// Scores where the logits were not kept.  A block streams a run of key tiles past
+// up to kScoreRows rows that stay in shared memory (more rows: once per such group); the
+// two halves of the softmax warps take the tiles in turn, each with its own half of tensor
+// memory, and a thread sums one key's weights over the rows, whose logs it knows.
+template <class T>
+__global__ void __launch_bounds__(kScoreThreads, 1)
+    attend_score_kernel(AttendArgs a, ScorePlan p, const T* q,
+                        const __grid_constant__ CUtensorMap k_map, const float* row_logs,
+                        const float* score_in, float* score_out) {
+    extern __shared__ char smem_raw[];
+    __shared__ uint64_t bars[2 * kMaxStages + 5];
+    __shared__ uint32_t s_tmem;
+    __shared__ alignas(16) float s_log[kScoreRows];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t bh = blockIdx.x / p.blocks;
+    const int b = (int)(bh / a.Hkv), h = (int)(bh % a.Hkv);
+    pdl_wait();
+    const int64_t n = cache_length(a, b);
+    // the sequence's tiles shared out evenly among its blocks
+    const int64_t all = (n + kTile - 1) / kTile, per = (all + p.blocks - 1) / p.blocks;
+    const int64_t first = blockIdx.x % p.blocks * per;
+    const int tiles = (int)(all - first < per ? all - first : per);
+    if (tiles <= 0) return;
+    const int subs = (a.D + 63) / 64;
+    const uint32_t sub_bytes = kTile * 128, tile_bytes = subs * sub_bytes;
+    const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u, q_at = ring + p.stages * tile_bytes;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages,
+                   q_full = empty + 8 * kMaxStages, done = q_full + 8, used = done + 16;
+    // groups of rows that see some key here: the first key sees the most rows
+    const int64_t past = first * kTile - (n - a.Sq);
+    const int64_t rg0 = (past > 0 ? past * a.G : 0) / kScoreRows,
+                  rgs = (a.R + kScoreRows - 1) / kScoreRows;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        mbar_init(q_full, 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(done + 8 * i, 1);
+            mbar_init(used + 8 * i, 128);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 1) tmem_alloc(smem_addr(&s_tmem), 2 * kScoreRows);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            int issued = 0;
+            for (int64_t rg = rg0; rg < rgs && ok; ++rg)
+                for (int t = 0; t < tiles; ++t, ++issued) {
+                    const int s = issued % p.stages, turn = issued / p.stages;
+                    if (turn > 0) ok = mbar_wait(empty + 8 * s, (turn - 1) & 1);
+                    if (!ok) break;
+                    mbar_expect(full + 8 * s, tile_bytes);
+                    for (int c = 0; c < subs; ++c)
+                        tma_load_4d(ring + s * tile_bytes + c * sub_bytes, &k_map, full + 8 * s, c * 64,
+                                    (int)((first + t) * kTile), h * a.kh, b * a.kb);
+                }
+            if (!ok)  // gave up: let the copies in flight land before the block ends
+                for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+                    mbar_wait(full + 8 * (i % p.stages), (i / p.stages) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int item = 0, turns[2] = {0, 0};
+            for (int64_t rg = rg0; rg < rgs && ok; ++rg) {
+                const int rows = (int)(a.R - rg * kScoreRows < kScoreRows ? a.R - rg * kScoreRows : kScoreRows);
+                const uint32_t shape = mma_shape(Pair<T>::bf16, false, false, kTile, (rows + 31) & ~31);
+                ok = mbar_wait(q_full, (rg - rg0) & 1);
+                for (int t = 0; t < tiles && ok; ++t, ++item) {
+                    const int s = item % p.stages, half = t & 1;
+                    ok = mbar_wait(full + 8 * s, (item / p.stages) & 1);
+                    if (ok && turns[half] > 0) ok = mbar_wait(used + 8 * half, (turns[half] - 1) & 1);
+                    if (!ok) break;
+                    ++turns[half];
+                    tc_fence_after();
+                    for (int kk = 0; kk * 16 < a.D; ++kk) {
+                        const uint32_t sub = kk >> 2, in = (kk & 3) * 32;
+                        mma_f16(tmem + half * kScoreRows,
+                                operand(ring + s * tile_bytes + sub * sub_bytes + in, 16, 1024, kSwizzle128),
+                                operand(q_at + sub * (kScoreRows * 128) + in, 16, 1024, kSwizzle128),
+                                shape, kk > 0);
+                    }
+                    mma_commit(empty + 8 * s);
+                    mma_commit(done + 8 * half);
+                }
+            }
+        }
+    } else {
+        const int quarter = warp & 3, half = (warp - 2) / 4, key = quarter * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + half * kScoreRows;
+        const float* in = score_in != nullptr ? score_in + b * a.sib + h * a.sih : nullptr;
+        float* out = score_out + b * a.sob + h * a.soh;
+        int turn = 0;
+        for (int64_t rg = rg0; rg < rgs; ++rg) {
+            const int64_t row0 = rg * kScoreRows;
+            const int rows = (int)(a.R - row0 < kScoreRows ? a.R - row0 : kScoreRows);
+            // both halves are done with the rows before, and with them the products
+            softmax_sync<256>();
+            load_rows<T, kScoreRows>(a, q, b, h, row0, rows, q_at, threadIdx.x - 64, 256);
+            for (int r = threadIdx.x - 64; r < kScoreRows; r += 256)
+                s_log[r] = r < rows ? row_logs[bh * a.R + row0 + r] : INFINITY;
+            fence_async_smem();
+            softmax_sync<256>();
+            mbar_arrive(q_full);
+            for (int t = half; t < tiles; t += 2) {
+                const int64_t j = (first + t) * kTile + key;
+                // rows from this one on (of the group) see the key
+                const int64_t past_j = j - (n - a.Sq);
+                const int64_t from64 = (past_j > 0 ? past_j * a.G : 0) - row0;
+                const int from = from64 <= 0 ? 0 : from64 < kScoreRows ? (int)from64 : kScoreRows;
+                float old = 0.f;
+                if (j < n) old = rg > rg0 ? out[j] : in != nullptr ? in[j] : 0.f;
+                if (ok) ok = mbar_wait(done + 8 * half, turn & 1);
+                ++turn;
+                ok = __all_sync(kAll, ok);
+                float s = 0.f;
+                if (ok) {
+                    tc_fence_after();
+                    for (int c = 0; c < rows; c += 32) {
+                        float x[32];
+                        tmem_ld<32>(lanes + c, x);
+                        if (__any_sync(kAll, from > c)) {
+#pragma unroll
+                            for (int r = 0; r < 32; ++r)
+                                s += c + r >= from ? ex2_ftz(fmaf(x[r], a.scale_log2, -s_log[c + r])) : 0.f;
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < 32; ++r)
+                                s += ex2_ftz(fmaf(x[r], a.scale_log2, -s_log[c + r]));
+                        }
+                    }
+                    tc_fence_before();
+                    mbar_arrive(used + 8 * half);
+                }
+                if (j < n) out[j] = ok ? old + s : NAN;  // a wait that ran out leaves NaN
+            }
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free(tmem, 2 * kScoreRows);
     }
 }
 
@@ -525,10 +710,28 @@ AttendPlan make_plan(int64_t B, int64_t Sq, int64_t Hq, int64_t Hkv, int64_t N, 
     if (splits < want) splits = want < tiles ? want : tiles;
     p.splits = (int)splits;
     p.tiles = (int)((tiles + splits - 1) / splits);
+    p.keep = R <= kKeepRows;
     p.RP = (R + 3) / 4 * 4;
-    p.off_part = up256((size_t)(bh * splits * R) * 8);
+    p.off_lse = up256((size_t)(bh * splits * R) * 8);
+    p.off_part = p.off_lse + up256((size_t)(bh * R) * 4);
     p.off_logits = p.off_part + up256((size_t)(bh * splits * R) * (size_t)D * 4);
-    p.bytes = p.off_logits + up256((size_t)(bh * N) * (size_t)p.RP * 4);
+    p.bytes = p.off_logits + (p.keep ? up256((size_t)(bh * N) * (size_t)p.RP * 4) : 0);
+    return p;
+}
+
+ScorePlan make_score_plan(int64_t bh, int64_t N, int64_t D) {
+    ScorePlan p{};
+    const int subs = (int)(D + 63) / 64, tile = subs * kTile * 128, fixed = 1024 + subs * kScoreRows * 128;
+    // two blocks an SM where two stages fit half of it
+    const bool two = fixed + 2 * tile <= 112 * 1024;
+    const int room = (two ? 112 : 224) * 1024 - fixed;
+    p.stages = room / tile < kMaxStages ? room / tile : kMaxStages;
+    p.smem = fixed + p.stages * tile;
+    const int64_t tiles = (N + kTile - 1) / kTile, slots = 148 * (two ? 2 : 1);
+    // one wave of blocks, or blocks of at most 16 tiles where there are more heads
+    int64_t blocks = slots / bh;
+    if (blocks < (tiles + 15) / 16 && bh * ((tiles + 15) / 16) > 2 * slots) blocks = (tiles + 15) / 16;
+    p.blocks = (int)(blocks < 1 ? 1 : blocks < tiles ? blocks : tiles);
     return p;
 }
 
@@ -574,17 +777,17 @@ bool cache_map(CUtensorMap* map, int dtype, const void* base, int64_t B, int64_t
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class T, int RT>
+template <class T, int RT, int CW>
 cudaError_t launch_split(const AttendArgs& a, const AttendPlan& p, const void* q,
                          const CUtensorMap& k, const CUtensorMap& v, float2* stats, float* part,
                          float* logits, cudaStream_t st) {
     static std::atomic<unsigned long long> done{0};
     once_per_device(done, [] {
-        cudaFuncSetAttribute(attend_split_kernel<T, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             225 * 1024);
+        cudaFuncSetAttribute(attend_split_kernel<T, RT, CW>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
     });
     const int64_t blocks = (int64_t)a.B * a.Hkv * p.splits * p.row_tiles;
-    return launch_pdl(attend_split_kernel<T, RT>, dim3((unsigned)blocks), dim3(kSplitThreads),
+    return launch_pdl(attend_split_kernel<T, RT, CW>, dim3((unsigned)blocks), dim3(64 + 128 * CW),
                       (size_t)p.smem, st, a, p, (const T*)q, k, v, stats, part, logits);
 }
 
@@ -593,24 +796,38 @@ cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& p, const void* 
                           const CUtensorMap& k, const CUtensorMap& v, char* ws,
                           const float* score_in, float* score_out, void* out, cudaStream_t st) {
     float2* stats = (float2*)ws;
+    float* row_logs = (float*)(ws + p.off_lse);
     float* part = (float*)(ws + p.off_part);
     float* logits = (float*)(ws + p.off_logits);
     cudaError_t e;
     {
         ProfScope prof("attend_split", st);
-        e = p.rt == 16   ? launch_split<T, 16>(a, p, q, k, v, stats, part, logits, st)
-            : p.rt == 32 ? launch_split<T, 32>(a, p, q, k, v, stats, part, logits, st)
-                         : launch_split<T, 64>(a, p, q, k, v, stats, part, logits, st);
+        e = p.rt == 16   ? launch_split<T, 16, 1>(a, p, q, k, v, stats, part, logits, st)
+            : p.rt == 32 ? launch_split<T, 32, 2>(a, p, q, k, v, stats, part, logits, st)
+                         : launch_split<T, 64, 2>(a, p, q, k, v, stats, part, logits, st);
     }
     if (e != cudaSuccess) return e;
-    ProfScope prof("attend_join", st);
-    const int key_blocks = (int)((a.N + kJoinThreads - 1) / kJoinThreads);
-    const int64_t score_blocks = (int64_t)a.B * a.Hkv * key_blocks;
     const int64_t rows = (int64_t)a.B * a.Hkv * a.R;
-    return launch_pdl(attend_join_kernel<T>, dim3((unsigned)(score_blocks + (rows + 7) / 8)),
-                      dim3(kJoinThreads), 0, st, a, p, score_blocks, key_blocks,
-                      (const float2*)stats, (const float*)part, (const float*)logits, score_in,
-                      score_out, (T*)out);
+    {
+        ProfScope prof("attend_join", st);
+        const int key_blocks = (int)((a.N + kJoinThreads - 1) / kJoinThreads);
+        const int64_t score_blocks = p.keep ? (int64_t)a.B * a.Hkv * key_blocks : 0;
+        e = launch_pdl(attend_join_kernel<T>, dim3((unsigned)(score_blocks + (rows + 7) / 8)),
+                       dim3(kJoinThreads), 0, st, a, p, score_blocks, key_blocks,
+                       (const float2*)stats, (const float*)part, (const float*)logits, score_in,
+                       score_out, row_logs, (T*)out);
+    }
+    if (e != cudaSuccess || p.keep) return e;
+    ProfScope prof("attend_score", st);
+    static std::atomic<unsigned long long> done{0};
+    once_per_device(done, [] {
+        cudaFuncSetAttribute(attend_score_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             224 * 1024);
+    });
+    const ScorePlan sp = make_score_plan((int64_t)a.B * a.Hkv, a.N, a.D);
+    return launch_pdl(attend_score_kernel<T>, dim3((unsigned)((int64_t)a.B * a.Hkv * sp.blocks)),
+                      dim3(kScoreThreads), (size_t)sp.smem, st, a, sp, (const T*)q, k,
+                      (const float*)row_logs, score_in, score_out);
 }
 
 }  // namespace
