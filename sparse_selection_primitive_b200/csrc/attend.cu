@@ -9,11 +9,10 @@
 // Keys take the M side of the matrix instruction: S^T = K Q^T is 128 keys x RT rows, so
 // that a few query rows (one token and its G heads) fill a whole instruction, each
 // thread holds one key's logits for all rows, and the column sums that the scores need are
-// sums inside a thread.  A block takes a run of key tiles small enough that all their
-// logits stay in tensor memory; it therefore knows the run's maximum before it forms any
-// weight, and O^T = V^T P (D x RT, V read as it lies) needs no rescaling.  Weights go to
+// sums inside a thread.  O^T = V^T P is D x RT, with V read as it lies.  Weights go to
 // the second product as pairs of 16-bit values, p = hi + lo, so that they keep 16 bits
-// and more of p.  Runs are joined by a second kernel, which also turns logits into scores.
+// and more of p.  Runs of key tiles are joined by a second kernel; scores come from kept
+// logits where few rows share a key, and from a second S^T where keeping them would cost more.
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -31,7 +30,7 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kTile = 128;          // keys per tile: the M of S^T
 constexpr int kKeepRows = 16;       // logits of more rows a key are formed again, not kept
 constexpr int kMaxStages = 6;
-constexpr int kMaxTiles = 32;
+constexpr int kRunTiles = 16;
 constexpr int kJoinThreads = 256;
 
 struct AttendArgs {
@@ -49,7 +48,6 @@ struct AttendPlan {
     int rt;         // rows per tile
     int row_tiles;
     int splits;     // runs of key tiles per row tile
-    int tiles;      // most key tiles per run
     int stages, cols, smem;
     int keep;       // the logits are kept for the scores
     int64_t RP;     // rows of logits per key, padded
@@ -150,24 +148,34 @@ struct Pair<__half> {
     }
 };
 
-// One run of key tiles for one tile of rows.  Writes the run's row maxima and sums
-// (stats), its unnormalised outputs (part) and, where they are kept, the logits, all in
+// One run of key tiles for one tile of rows.  Writes the rows' references and sums
+// (stats), the unnormalised outputs (part) and, where they are kept, the logits, all in
 // fp32.  Warp 0 loads, warp 1 multiplies, and 4 CW warps do the softmax: a warp can read
 // one quarter of the lanes of tensor memory, and CW warps share the rows of a quarter.
+//
+// Weights are 2^(x - m) with a reference m per row that is the exact maximum of the first
+// tile and is raised only when some logit passes it by kSlack: a maximum over the keys is a
+// maximum across threads, dear to form for every tile, and any reference within a factor
+// 2^kSlack of it serves as well (p <= 2^kSlack stays far inside fp16, and relative errors
+// are the same).  Raising it rescales the sums and the outputs in tensor memory.
 template <class T, int RT, int CW>
-__global__ void __launch_bounds__(64 + 128 * CW, 1)
+__global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
     attend_split_kernel(AttendArgs a, AttendPlan p, const T* q,
                         const __grid_constant__ CUtensorMap k_map,
                         const __grid_constant__ CUtensorMap v_map, float2* stats, float* part,
                         float* logits) {
-    extern __shared__ char smem_raw[];
-    __shared__ uint64_t bars[2 * kMaxStages + kMaxTiles + 2];
-    __shared__ uint32_t s_tmem;
-    __shared__ int s_failed;
     constexpr int RC = RT / CW;  // rows of a softmax warp
     constexpr int kSoftmax = 128 * CW;
+    constexpr float kSlack = 12.f;
+    extern __shared__ char smem_raw[];
+    __shared__ uint64_t bars[2 * kMaxStages + 4];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_failed;
     __shared__ float red[4][RT];
-    __shared__ alignas(16) float s_max[RT];
+    // per row: the reference (0 while no key was seen), and what raising it last time
+    // added to logits and multiplied sums with; per half: how far a logit may pass it
+    __shared__ alignas(16) float s_ref[RT], s_shift[RT], s_scale[RT];
+    __shared__ float s_slack[CW];
     __shared__ alignas(16) int s_lim[RT];  // keys that each row sees, from the run's first
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rt = blockIdx.x % p.row_tiles;
@@ -199,23 +207,27 @@ __global__ void __launch_bounds__(64 + 128 * CW, 1)
     const uint32_t q_at = ring + p.stages * stage_bytes;
     const uint32_t p_at = q_at + subs * RT * 128;       // hi, then lo
     const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages,
-                   s_done = empty + 8 * kMaxStages, p_full = s_done + 8 * kMaxTiles,
-                   p_empty = p_full + 8;
+                   s_done = empty + 8 * kMaxStages, p_full = s_done + 16, p_empty = p_full + 8;
     if (threadIdx.x == 0) {
         for (int i = 0; i < p.stages; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
         }
-        for (int i = 0; i < tiles; ++i) mbar_init(s_done + 8 * i, 1);
+        mbar_init(s_done, 1);
+        mbar_init(s_done + 8, 1);
         mbar_init(p_full, kSoftmax);
         mbar_init(p_empty, 1);
         fence_barrier_init();
         s_failed = 0;
     }
     if (threadIdx.x < RT) {
+        const int most = tiles * kTile;
         int64_t lim = n - a.Sq + 1 + (row0 + threadIdx.x) / a.G - first * kTile;
         lim = lim < 0 ? 0 : lim;
-        s_lim[threadIdx.x] = (int)(threadIdx.x < rows && lim < tiles * kTile ? lim : tiles * kTile);
+        s_ref[threadIdx.x] = 0.f;
+        s_shift[threadIdx.x] = -INFINITY;
+        if (threadIdx.x < CW) s_slack[threadIdx.x] = -INFINITY;
+        s_lim[threadIdx.x] = (int)(threadIdx.x < rows && lim < most ? lim : most);
     }
     if (warp == 1) tmem_alloc(smem_addr(&s_tmem), p.cols);
     load_rows<T, RT>(a, q, b, h, row0, rows, q_at, threadIdx.x, 64 + kSoftmax);
@@ -223,20 +235,25 @@ __global__ void __launch_bounds__(64 + 128 * CW, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem, o_col = tmem + tiles * RT;
-    const int items = 2 * tiles;  // the run's key tiles, then its value tiles
+    // logits of two tiles, then the outputs
+    const uint32_t tmem = s_tmem, o_col = tmem + 2 * RT;
+    // the ring's items: K0, K1, V0, K2, V1, ..., V(last)
+    const int items = 2 * tiles;
+    auto key_item = [](int t) { return t == 0 ? 0 : 2 * t - 1; };
+    auto value_item = [&](int t) { return t + 1 < tiles ? 2 * t + 2 : 2 * t + 1; };
     bool ok = true;
 
     if (warp == 0) {
         if (lane == 0) {
             int issued = 0;
-            for (; issued < items && ok; ++issued) {
+            for (; issued < items; ++issued) {
                 const int s = issued % p.stages, turn = issued / p.stages;
                 if (turn > 0) ok = mbar_wait(empty + 8 * s, (turn - 1) & 1);
                 if (!ok) break;
                 mbar_expect(full + 8 * s, stage_bytes);
-                const bool key = issued < tiles;
-                const int y = (int)((first + (key ? issued : issued - tiles)) * kTile);
+                const bool key = issued == 0 || (issued % 2 == 1 && issued < items - 1);
+                const int t = key ? (issued + 1) / 2 : (issued - 1) / 2;
+                const int y = (int)((first + t) * kTile);
                 for (int c = 0; c < subs; ++c)
                     tma_load_4d(ring + s * stage_bytes + c * sub_bytes, key ? &k_map : &v_map,
                                 full + 8 * s, c * 64, y, h * (key ? a.kh : a.vh),
@@ -250,23 +267,24 @@ __global__ void __launch_bounds__(64 + 128 * CW, 1)
         if (lane == 0) {
             const uint32_t shape_s = mma_shape(Pair<T>::bf16, false, false, kTile, RT);
             const uint32_t shape_o = mma_shape(Pair<T>::bf16, true, true, 128, RT);
-            for (int t = 0; t < tiles && ok; ++t) {
-                const int s = t % p.stages;
-                ok = mbar_wait(full + 8 * s, (t / p.stages) & 1);
-                if (!ok) break;
+            auto logits_of = [&](int t) {  // S^T of tile t into its half
+                const int item = key_item(t), s = item % p.stages;
+                if (!mbar_wait(full + 8 * s, (item / p.stages) & 1)) return false;
                 tc_fence_after();
                 for (int kk = 0; kk * 16 < a.D; ++kk) {
                     const uint32_t sub = kk >> 2, in = (kk & 3) * 32;
-                    mma_f16(tmem + t * RT,
+                    mma_f16(tmem + (t & 1) * RT,
                             operand(ring + s * stage_bytes + sub * sub_bytes + in, 16, 1024, kSwizzle128),
                             operand(q_at + sub * (RT * 128) + in, 16, 1024, kSwizzle128), shape_s,
                             kk > 0);
                 }
                 mma_commit(empty + 8 * s);
-                mma_commit(s_done + 8 * t);
-            }
+                mma_commit(s_done + 8 * (t & 1));
+                return true;
+            };
+            ok = logits_of(0) && (tiles == 1 || logits_of(1));
             for (int t = 0; t < tiles && ok; ++t) {
-                const int item = tiles + t, s = item % p.stages;
+                const int item = value_item(t), s = item % p.stages;
                 ok = mbar_wait(full + 8 * s, (item / p.stages) & 1) && mbar_wait(p_full, t & 1);
                 if (!ok) break;
                 tc_fence_after();
@@ -281,74 +299,119 @@ __global__ void __launch_bounds__(64 + 128 * CW, 1)
                     }
                 mma_commit(empty + 8 * s);
                 mma_commit(p_empty);
+                // the softmax has read tile t's half
+                if (t + 2 < tiles) ok = logits_of(t + 2);
             }
         }
     } else {
         const int quarter = warp & 3;                  // the lanes of tensor memory it may read
         const int key = quarter * 32 + lane;           // of a tile
-        const int c0 = (warp - 2) / 4 * RC;            // its first row
+        const int group = (warp - 2) / 4, c0 = group * RC;  // its first row
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
-        const int tid = threadIdx.x - 64;
-        float top[RC];
-#pragma unroll
-        for (int r = 0; r < RC; ++r) top[r] = -INFINITY;
-        // phase 1: logits, their maxima
-        for (int t = 0; t < tiles && ok; ++t) {
-            ok = mbar_wait(s_done + 8 * t, 0);
-            if (!__all_sync(kAll, ok)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            float x[RC];
-            tmem_ld<RC>(lanes + t * RT, x);
-            const int64_t j = (first + t) * kTile + key;
-            const bool whole = (t + 1) * kTile <= s_lim[0];  // the first row sees the fewest
-#pragma unroll
-            for (int r = 0; r < RC; ++r) {
-                x[r] *= a.scale_log2;
-                if (!whole && t * kTile + key >= s_lim[c0 + r]) x[r] = -INFINITY;
-                top[r] = fmaxf(top[r], x[r]);
-            }
-            if (p.keep && j < n) {
-                float* to = logits + (bh * a.N + j) * p.RP + row0 + c0;
-#pragma unroll
-                for (int r = 0; r < RC; r += 4)
-                    if (row0 + c0 + r < p.RP)
-                        *reinterpret_cast<float4*>(to + r) =
-                            make_float4(x[r], x[r + 1], x[r + 2], x[r + 3]);
-            }
-        }
-        join_lanes<RC>(top, lane, [](float u, float w) { return fmaxf(u, w); });
-        constexpr int kOwn = RC > 32 ? RC / 32 : 1;
-        const int at = joined_at<RC>(lane);
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) red[quarter][c0 + at + i] = top[i];
-        softmax_sync<kSoftmax>();
-        if (tid < RT) {
-            const float m = fmaxf(fmaxf(red[0][tid], red[1][tid]), fmaxf(red[2][tid], red[3][tid]));
-            s_max[tid] = m == -INFINITY ? 0.f : m;
-        }
-        softmax_sync<kSoftmax>();
-        // phase 2: weights relative to the run's maximum
+        const int own = joined_at<RC>(lane);
         float sum[RC];
 #pragma unroll
         for (int r = 0; r < RC; ++r) sum[r] = 0.f;
-        for (int t = 0; t < tiles && ok; ++t) {
+        for (int t = 0; t < tiles; ++t) {
+            ok = ok && mbar_wait(s_done + 8 * (t & 1), (t >> 1) & 1);
+            ok = __all_sync(kAll, ok);
+            tc_fence_after();
             float x[RC];
-            tmem_ld<RC>(lanes + t * RT, x);
+            tmem_ld<RC>(lanes + (t & 1) * RT, x);
             const int64_t j0 = (first + t) * kTile, j = j0 + key;
-            const bool whole = (t + 1) * kTile <= s_lim[0];
+            if ((t + 1) * kTile > s_lim[0]) {  // the first row sees the fewest
+                const int at = t * kTile + key;
+#pragma unroll
+                for (int r = 0; r < RC; ++r)
+                    if (at >= s_lim[c0 + r]) x[r] = -INFINITY;
+            }
+            const float slack = s_slack[group];
+            bool past = false;
+            if constexpr (RT == kKeepRows) {
+#pragma unroll
+                for (int r = 0; r < RC; ++r)  // -inf stays -inf whatever the scale
+                    x[r] = x[r] == -INFINITY ? x[r] : x[r] * a.scale_log2;
+                if (j < n) {
+                    float* to = logits + (bh * a.N + j) * p.RP + row0 + c0;
+#pragma unroll
+                    for (int r = 0; r < RC; r += 4)
+                        if (row0 + c0 + r < p.RP)
+                            *reinterpret_cast<float4*>(to + r) =
+                                make_float4(x[r], x[r + 1], x[r + 2], x[r + 3]);
+                }
+#pragma unroll
+                for (int r = 0; r < RC; ++r) x[r] -= s_ref[c0 + r];
+            } else {
+#pragma unroll
+                for (int r = 0; r < RC; ++r)
+                    x[r] = x[r] == -INFINITY ? x[r] : fmaf(x[r], a.scale_log2, -s_ref[c0 + r]);
+            }
+#pragma unroll
+            for (int r = 0; r < RC; ++r) past |= x[r] > slack;
+            // one answer for the four warps that share these rows
+            uint32_t raise;
+            asm volatile(
+                "{\n\t.reg .pred u, v;\n\tsetp.ne.u32 u, %1, 0;\n\t"
+                "barrier.cta.red.or.pred v, %2, 128, u;\n\tselp.u32 %0, 1, 0, v;\n\t}"
+                : "=r"(raise)
+                : "r"(past ? 1u : 0u), "r"(2 + group)
+                : "memory");
+            // the outputs so far are complete, and the weights' room is free
+            bool ready = t == 0;
+            if (raise) {
+                if (!ready) {
+                    ok = ok && mbar_wait(p_empty, (t - 1) & 1);
+                    ok = __all_sync(kAll, ok);
+                    tc_fence_after();
+                    ready = true;
+                }
+                {
+                    float top[RC];
+#pragma unroll
+                    for (int r = 0; r < RC; ++r) top[r] = x[r];
+                    join_lanes<RC>(top, lane, [](float u, float w) { return fmaxf(u, w); });
+                    red[quarter][c0 + own] = top[0];
+                }
+                asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
+                if (key < 32) {
+                    bool unseen = false;
+                    if (key < RC) {
+                        const int c = c0 + key;
+                        const float over = fmaxf(fmaxf(red[0][c], red[1][c]), fmaxf(red[2][c], red[3][c]));
+                        const bool fresh = s_shift[c] == -INFINITY;  // nothing seen before
+                        unseen = fresh && over == -INFINITY;
+                        const float up = unseen ? 0.f : fresh ? over : fmaxf(over, 0.f);
+                        s_ref[c] += up;
+                        s_scale[c] = fresh ? 0.f : ex2_ftz(-up);
+                        s_shift[c] = unseen ? -INFINITY : -up;
+                    }
+                    unseen = __any_sync(kAll, unseen);
+                    if (key == 0) s_slack[group] = unseen ? -INFINITY : kSlack;
+                }
+                asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
+#pragma unroll
+                for (int r = 0; r < RC; ++r) {
+                    x[r] += s_shift[c0 + r];
+                    sum[r] *= s_scale[c0 + r];
+                }
+                if (t > 0)
+                    for (int m = 0; m * 128 < a.D; ++m) {
+                        float o[RC];
+                        tmem_ld<RC>(lanes + 2 * RT + m * RT, o);
+#pragma unroll
+                        for (int r = 0; r < RC; ++r) o[r] *= s_scale[c0 + r];
+                        tmem_st<RC>(lanes + 2 * RT + m * RT, o);
+                    }
+            }
 #pragma unroll
             for (int r = 0; r < RC; ++r) {
-                x[r] = ex2_ftz(__fmul_rn(x[r], a.scale_log2) - s_max[c0 + r]);
-                if (!whole && t * kTile + key >= s_lim[c0 + r]) x[r] = 0.f;
+                x[r] = ex2_ftz(x[r]);
                 sum[r] += x[r];
             }
-            if (t > 0) ok = mbar_wait(p_empty, (t - 1) & 1);
-            if (j0 + kTile > n && c0 == 0) {
+            if (!ready) ok = ok && mbar_wait(p_empty, (t - 1) & 1);
+            if (j0 + kTile > n && group == 0) {
                 // value rows behind the cache's end may hold anything: 0 x NaN is NaN
-                const int item = tiles + t, s = item % p.stages;
+                const int item = value_item(t), s = item % p.stages;
                 ok = ok && mbar_wait(full + 8 * s, (item / p.stages) & 1);
                 if (j >= n)
                     for (int c = 0; c < subs * 8; ++c)
@@ -357,10 +420,6 @@ __global__ void __launch_bounds__(64 + 128 * CW, 1)
                                          (c & 7) * 16),
                                      "r"(0)
                                      : "memory");
-            }
-            if (!__all_sync(kAll, ok)) {
-                ok = false;
-                break;
             }
 #pragma unroll
             for (int r = 0; r < RC; r += 8) {
@@ -387,21 +446,21 @@ __global__ void __launch_bounds__(64 + 128 * CW, 1)
         join_lanes<RC>(sum, lane, [](float u, float w) { return u + w; });
         if (ok) ok = mbar_wait(p_empty, (tiles - 1) & 1);
         if (!ok) s_failed = 1;
-#pragma unroll
-        for (int i = 0; i < kOwn; ++i) red[quarter][c0 + at + i] = sum[i];
+        red[quarter][c0 + own] = sum[0];
         softmax_sync<kSoftmax>();
         tc_fence_after();
+        const int tid = threadIdx.x - 64;
         if (tid < rows) {
             const float l = red[0][tid] + red[1][tid] + red[2][tid] + red[3][tid];
             // a wait that ran out leaves NaN, which the answer then shows
             my_stats[tid] = s_failed ? make_float2(NAN, NAN)
-                            : l > 0.f || isnan(l) ? make_float2(s_max[tid], l)
+                            : l > 0.f || isnan(l) ? make_float2(s_ref[tid], l)
                                                   : make_float2(-INFINITY, 0.f);
         }
         if (!s_failed)
             for (int m = 0; m * 128 < a.D; ++m) {
                 float o[RC];
-                tmem_ld<RC>(lanes + tiles * RT + m * RT, o);
+                tmem_ld<RC>(lanes + 2 * RT + m * RT, o);
                 const int d = m * 128 + key;
                 if (d < a.D) {
                     float* to = part + ((bh * p.splits + split) * a.R + row0 + c0) * a.D + d;
@@ -688,33 +747,27 @@ AttendPlan make_plan(int64_t B, int64_t Sq, int64_t Hq, int64_t Hkv, int64_t N, 
     const int64_t R = Sq * (Hq / Hkv), bh = B * Hkv;
     p.rt = R <= 16 ? 16 : R <= 32 ? 32 : 64;
     p.row_tiles = (int)((R + p.rt - 1) / p.rt);
-    const int subs = (int)(D + 63) / 64, stage = subs * kTile * 128, o_cols = (int)(D + 127) / 128 * p.rt;
-    // two blocks an SM where rows and weights leave room for three stages in half of it
-    const int fixed = subs * p.rt * 128 + p.rt * 512 + 1024;
+    p.keep = R <= kKeepRows;
+    p.cols = 4 * p.rt;  // two tiles of logits, outputs of up to 256 columns
+    const int subs = (int)(D + 63) / 64, stage = subs * kTile * 128;
+    // V^T is read 128 rows at a time: past an odd last block of 64 columns its (unused) rows
+    // are whatever follows, which has to be there
+    const int fixed = 1024 + subs * p.rt * 128 + p.rt * 512 + (subs % 2 ? kTile * 128 : 0);
+    // two blocks an SM where three stages fit half of it
     const bool two = fixed + 3 * stage <= 112 * 1024;
-    p.cols = two ? 256 : 512;
-    // one block of 64 columns more than the ring holds may be read as (unused) rows of V^T
     const int room = (two ? 112 : 224) * 1024 - fixed;
     p.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
-    p.smem = p.stages * stage + fixed + (subs % 2 ? kTile * 128 : 0);
-    while (p.smem > (two ? 112 : 224) * 1024) {
-        --p.stages;
-        p.smem -= stage;
-    }
-    const int cap = (p.cols - o_cols) / p.rt;
-    const int64_t tiles = (N + kTile - 1) / kTile;
-    const int64_t most = cap < kMaxTiles ? cap : kMaxTiles;
-    int64_t splits = (tiles + most - 1) / most;
-    // enough blocks to fill 148 SMs
-    const int64_t want = (148 * (two ? 2 : 1) + bh * p.row_tiles - 1) / (bh * p.row_tiles);
-    if (splits < want) splits = want < tiles ? want : tiles;
-    p.splits = (int)splits;
-    p.tiles = (int)((tiles + splits - 1) / splits);
-    p.keep = R <= kKeepRows;
+    p.smem = fixed + p.stages * stage;
+    // Runs: enough blocks for every slot of 148 SMs, and with many heads runs of at most
+    // kRunTiles tiles, so that the last blocks to start are short
+    const int64_t tiles = (N + kTile - 1) / kTile, slots = 148 * (two ? 2 : 1);
+    int64_t splits = (slots + bh * p.row_tiles - 1) / (bh * p.row_tiles);
+    if (splits < (tiles + kRunTiles - 1) / kRunTiles) splits = (tiles + kRunTiles - 1) / kRunTiles;
+    p.splits = (int)(splits < tiles ? splits : tiles);
     p.RP = (R + 3) / 4 * 4;
-    p.off_lse = up256((size_t)(bh * splits * R) * 8);
+    p.off_lse = up256((size_t)(bh * p.splits * R) * 8);
     p.off_part = p.off_lse + up256((size_t)(bh * R) * 4);
-    p.off_logits = p.off_part + up256((size_t)(bh * splits * R) * (size_t)D * 4);
+    p.off_logits = p.off_part + up256((size_t)(bh * p.splits * R) * (size_t)D * 4);
     p.bytes = p.off_logits + (p.keep ? up256((size_t)(bh * N) * (size_t)p.RP * 4) : 0);
     return p;
 }
