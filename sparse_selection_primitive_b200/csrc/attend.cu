@@ -31,6 +31,7 @@ constexpr int kTile = 128;          // keys per tile: the M of S^T
 constexpr int kKeepRows = 16;       // logits of more rows a key are formed again, not kept
 constexpr int kMaxStages = 6;
 constexpr int kRunTiles = 16;
+constexpr int kBlockSmem = 223;     // KB of dynamic shared memory of a block that has an SM to itself
 constexpr int kJoinThreads = 256;
 
 struct AttendArgs {
@@ -129,22 +130,47 @@ __device__ __forceinline__ void load_rows(const AttendArgs& a, const T* q, int b
     }
 }
 
+// S^T = K Q^T of one tile: D / 16 steps along the rows of both operands, whose 128-byte
+// column blocks lie a tile of keys, or RT rows, apart.  One thread issues them, so it
+// only adds to the operands' descriptors: building one for each step took four times as
+// long as the step itself.
+template <int RT>
+__device__ __forceinline__ void key_products(uint32_t to, uint64_t k, uint64_t q, int D,
+                                             uint32_t shape) {
+    for (int sub = 0; sub * 64 < D; ++sub) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+            if (sub * 64 + kk * 16 < D)
+                mma_f16(to, k + advance(kk * 32), q + advance(kk * 32), shape, sub + kk > 0);
+        k += advance(kTile * 128);
+        q += advance(RT * 128);
+    }
+}
+
+// Two weights as words of two 16-bit values each: hi + lo = the weights to 16 bits and more.
 template <class T>
-struct Pair;  // two 16-bit values in a word
+struct Pair;
 template <>
 struct Pair<__nv_bfloat16> {
     static constexpr bool bf16 = true;
-    static __device__ __forceinline__ uint32_t pack(float a, float b) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&p);
+    // hi is cut off (a byte permutation; conversions run at a quarter of the rate), which
+    // leaves lo up to 2^-7 of the weight; lo is rounded: off by 2^-15 of it at most
+    static __device__ __forceinline__ void split(float a, float b, uint32_t* hi, uint32_t* lo) {
+        const uint32_t u = __float_as_uint(a), v = __float_as_uint(b);
+        *hi = __byte_perm(u, v, 0x7632);
+        const __nv_bfloat162 l =
+            __floats2bfloat162_rn(a - __uint_as_float(u & 0xffff0000u), b - __uint_as_float(v & 0xffff0000u));
+        *lo = *reinterpret_cast<const uint32_t*>(&l);
     }
 };
 template <>
 struct Pair<__half> {
     static constexpr bool bf16 = false;
-    static __device__ __forceinline__ uint32_t pack(float a, float b) {
-        const __half2 p = __floats2half2_rn(a, b);
-        return *reinterpret_cast<const uint32_t*>(&p);
+    static __device__ __forceinline__ void split(float a, float b, uint32_t* hi, uint32_t* lo) {
+        const __half2 h = __floats2half2_rn(a, b);
+        const __half2 l = __floats2half2_rn(a - __low2float(h), b - __high2float(h));
+        *hi = *reinterpret_cast<const uint32_t*>(&h);
+        *lo = *reinterpret_cast<const uint32_t*>(&l);
     }
 };
 
@@ -172,9 +198,10 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
     __shared__ uint32_t s_tmem;
     __shared__ int s_failed;
     __shared__ float red[4][RT];
-    // per row: the reference (0 while no key was seen), and what raising it last time
-    // added to logits and multiplied sums with; per half: how far a logit may pass it
-    __shared__ alignas(16) float s_ref[RT], s_shift[RT], s_scale[RT];
+    // per row: the reference (0 while no key was seen) and what raising it last time
+    // multiplied sums with; per group of rows: how far a logit may pass it
+    __shared__ alignas(16) float s_ref[RT], s_scale[RT];
+    __shared__ bool s_seen[RT];
     __shared__ float s_slack[CW];
     __shared__ alignas(16) int s_lim[RT];  // keys that each row sees, from the run's first
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -225,7 +252,7 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
         int64_t lim = n - a.Sq + 1 + (row0 + threadIdx.x) / a.G - first * kTile;
         lim = lim < 0 ? 0 : lim;
         s_ref[threadIdx.x] = 0.f;
-        s_shift[threadIdx.x] = -INFINITY;
+        s_seen[threadIdx.x] = false;
         if (threadIdx.x < CW) s_slack[threadIdx.x] = -INFINITY;
         s_lim[threadIdx.x] = (int)(threadIdx.x < rows && lim < most ? lim : most);
     }
@@ -235,7 +262,7 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // logits of two tiles, then the outputs
+    // logits of two tiles, then the outputs of the weights' hi and lo parts
     const uint32_t tmem = s_tmem, o_col = tmem + 2 * RT;
     // the ring's items: K0, K1, V0, K2, V1, ..., V(last)
     const int items = 2 * tiles;
@@ -266,18 +293,16 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
     } else if (warp == 1) {
         if (lane == 0) {
             const uint32_t shape_s = mma_shape(Pair<T>::bf16, false, false, kTile, RT);
-            const uint32_t shape_o = mma_shape(Pair<T>::bf16, true, true, 128, RT);
+            const uint32_t shape_o = mma_shape(Pair<T>::bf16, true, true, 128, 2 * RT);
+            const uint64_t q_op = operand(q_at, 16, 1024, kSwizzle128);
+            const uint64_t p_op = operand(p_at, 128, 2048, kNoSwizzle);
             auto logits_of = [&](int t) {  // S^T of tile t into its half
                 const int item = key_item(t), s = item % p.stages;
                 if (!mbar_wait(full + 8 * s, (item / p.stages) & 1)) return false;
                 tc_fence_after();
-                for (int kk = 0; kk * 16 < a.D; ++kk) {
-                    const uint32_t sub = kk >> 2, in = (kk & 3) * 32;
-                    mma_f16(tmem + (t & 1) * RT,
-                            operand(ring + s * stage_bytes + sub * sub_bytes + in, 16, 1024, kSwizzle128),
-                            operand(q_at + sub * (RT * 128) + in, 16, 1024, kSwizzle128), shape_s,
-                            kk > 0);
-                }
+                key_products<RT>(tmem + (t & 1) * RT,
+                                 operand(ring + s * stage_bytes, 16, 1024, kSwizzle128), q_op, a.D,
+                                 shape_s);
                 mma_commit(empty + 8 * s);
                 mma_commit(s_done + 8 * (t & 1));
                 return true;
@@ -288,15 +313,14 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
                 ok = mbar_wait(full + 8 * s, (item / p.stages) & 1) && mbar_wait(p_full, t & 1);
                 if (!ok) break;
                 tc_fence_after();
-                for (int m = 0; m * 128 < a.D; ++m)
-                    for (int kk = 0; kk < kTile / 16; ++kk) {
-                        const uint64_t v = operand(ring + s * stage_bytes + m * 2 * sub_bytes + kk * 2048,
-                                                   sub_bytes, 1024, kSwizzle128);
-                        for (int half = 0; half < 2; ++half)
-                            mma_f16(o_col + m * RT, v,
-                                    operand(p_at + half * (RT * 256) + kk * 256, 128, 2048, kNoSwizzle),
-                                    shape_o, t + kk + half > 0);
-                    }
+                for (int m = 0; m * 128 < a.D; ++m) {
+                    const uint64_t v = operand(ring + s * stage_bytes + m * 2 * sub_bytes, sub_bytes,
+                                               1024, kSwizzle128);
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        mma_f16(o_col + m * 2 * RT, v + advance(kk * 2048), p_op + advance(kk * 256),
+                                shape_o, t + kk > 0);
+                }
                 mma_commit(empty + 8 * s);
                 mma_commit(p_empty);
                 // the softmax has read tile t's half
@@ -308,7 +332,7 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
         const int key = quarter * 32 + lane;           // of a tile
         const int group = (warp - 2) / 4, c0 = group * RC;  // its first row
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
-        const int own = joined_at<RC>(lane);
+        constexpr int kPart = RC < 16 ? RC : 16;       // rows in registers at a time
         float sum[RC];
 #pragma unroll
         for (int r = 0; r < RC; ++r) sum[r] = 0.f;
@@ -316,38 +340,47 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
             ok = ok && mbar_wait(s_done + 8 * (t & 1), (t >> 1) & 1);
             ok = __all_sync(kAll, ok);
             tc_fence_after();
-            float x[RC];
-            tmem_ld<RC>(lanes + (t & 1) * RT, x);
             const int64_t j0 = (first + t) * kTile, j = j0 + key;
-            if ((t + 1) * kTile > s_lim[0]) {  // the first row sees the fewest
-                const int at = t * kTile + key;
+            const bool whole = (t + 1) * kTile <= s_lim[0];  // the first row sees the fewest
+            // the logits of kPart rows from c on, less the rows' references where asked
+            const auto part_of = [&](int c, float (&x)[kPart], bool keep) {
+                tmem_ld<kPart>(lanes + (t & 1) * RT + c, x);
+                const int r0 = c0 + c;
+                if (RT == kKeepRows) {
 #pragma unroll
-                for (int r = 0; r < RC; ++r)
-                    if (at >= s_lim[c0 + r]) x[r] = -INFINITY;
-            }
-            const float slack = s_slack[group];
-            bool past = false;
-            if constexpr (RT == kKeepRows) {
+                    for (int r = 0; r < kPart; ++r) x[r] *= a.scale_log2;
+                } else {
 #pragma unroll
-                for (int r = 0; r < RC; ++r)  // -inf stays -inf whatever the scale
-                    x[r] = x[r] == -INFINITY ? x[r] : x[r] * a.scale_log2;
-                if (j < n) {
-                    float* to = logits + (bh * a.N + j) * p.RP + row0 + c0;
-#pragma unroll
-                    for (int r = 0; r < RC; r += 4)
-                        if (row0 + c0 + r < p.RP)
-                            *reinterpret_cast<float4*>(to + r) =
-                                make_float4(x[r], x[r + 1], x[r + 2], x[r + 3]);
+                    for (int r = 0; r < kPart; ++r) x[r] = fmaf(x[r], a.scale_log2, -s_ref[r0 + r]);
                 }
+                if (!whole) {
+                    const int at = t * kTile + key;
 #pragma unroll
-                for (int r = 0; r < RC; ++r) x[r] -= s_ref[c0 + r];
-            } else {
+                    for (int r = 0; r < kPart; ++r)
+                        if (at >= s_lim[r0 + r]) x[r] = -INFINITY;
+                }
+                if (RT == kKeepRows) {
+                    if (keep && j < n) {
+                        float* to = logits + (bh * a.N + j) * p.RP + row0 + r0;
 #pragma unroll
-                for (int r = 0; r < RC; ++r)
-                    x[r] = x[r] == -INFINITY ? x[r] : fmaf(x[r], a.scale_log2, -s_ref[c0 + r]);
+                        for (int r = 0; r < kPart; r += 4)
+                            if (row0 + r0 + r < p.RP)
+                                *reinterpret_cast<float4*>(to + r) =
+                                    make_float4(x[r], x[r + 1], x[r + 2], x[r + 3]);
+                    }
+#pragma unroll
+                    for (int r = 0; r < kPart; ++r) x[r] -= s_ref[r0 + r];
+                }
+            };
+            float over[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < RC; c += kPart) {
+                float x[kPart];
+                part_of(c, x, true);
+#pragma unroll
+                for (int r = 0; r < kPart; ++r) over[r & 3] = fmaxf(over[r & 3], x[r]);
             }
-#pragma unroll
-            for (int r = 0; r < RC; ++r) past |= x[r] > slack;
+            const bool past = fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > s_slack[group];
             // one answer for the four warps that share these rows
             uint32_t raise;
             asm volatile(
@@ -365,48 +398,42 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
                     tc_fence_after();
                     ready = true;
                 }
-                {
-                    float top[RC];
-#pragma unroll
-                    for (int r = 0; r < RC; ++r) top[r] = x[r];
-                    join_lanes<RC>(top, lane, [](float u, float w) { return fmaxf(u, w); });
-                    red[quarter][c0 + own] = top[0];
+#pragma unroll 1
+                for (int c = 0; c < RC; c += kPart) {
+                    float x[kPart];
+                    part_of(c, x, false);
+                    join_lanes<kPart>(x, lane, [](float u, float w) { return fmaxf(u, w); });
+                    red[quarter][c0 + c + joined_at<kPart>(lane)] = x[0];
                 }
                 asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
                 if (key < 32) {
                     bool unseen = false;
                     if (key < RC) {
                         const int c = c0 + key;
-                        const float over = fmaxf(fmaxf(red[0][c], red[1][c]), fmaxf(red[2][c], red[3][c]));
-                        const bool fresh = s_shift[c] == -INFINITY;  // nothing seen before
-                        unseen = fresh && over == -INFINITY;
-                        const float up = unseen ? 0.f : fresh ? over : fmaxf(over, 0.f);
+                        const float by = fmaxf(fmaxf(red[0][c], red[1][c]), fmaxf(red[2][c], red[3][c]));
+                        unseen = !s_seen[c] && by == -INFINITY;
+                        const float up = unseen ? 0.f : s_seen[c] ? fmaxf(by, 0.f) : by;
                         s_ref[c] += up;
-                        s_scale[c] = fresh ? 0.f : ex2_ftz(-up);
-                        s_shift[c] = unseen ? -INFINITY : -up;
+                        s_scale[c] = s_seen[c] ? ex2_ftz(-up) : 0.f;
+                        s_seen[c] = !unseen;
                     }
                     unseen = __any_sync(kAll, unseen);
                     if (key == 0) s_slack[group] = unseen ? -INFINITY : kSlack;
                 }
                 asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
 #pragma unroll
-                for (int r = 0; r < RC; ++r) {
-                    x[r] += s_shift[c0 + r];
-                    sum[r] *= s_scale[c0 + r];
-                }
+                for (int r = 0; r < RC; ++r) sum[r] *= s_scale[c0 + r];
                 if (t > 0)
-                    for (int m = 0; m * 128 < a.D; ++m) {
-                        float o[RC];
-                        tmem_ld<RC>(lanes + 2 * RT + m * RT, o);
+#pragma unroll 1
+                    for (int c = 0; c < (a.D + 127) / 128 * 2 * RC; c += kPart) {
+                        // hi and lo parts of the outputs, of the first and the second 128 columns
+                        const int at = c % RC;
+                        float o[kPart];
+                        tmem_ld<kPart>(lanes + 2 * RT + c / RC * RT + at, o);
 #pragma unroll
-                        for (int r = 0; r < RC; ++r) o[r] *= s_scale[c0 + r];
-                        tmem_st<RC>(lanes + 2 * RT + m * RT, o);
+                        for (int r = 0; r < kPart; ++r) o[r] *= s_scale[c0 + at + r];
+                        tmem_st<kPart>(lanes + 2 * RT + c / RC * RT + at, o);
                     }
-            }
-#pragma unroll
-            for (int r = 0; r < RC; ++r) {
-                x[r] = ex2_ftz(x[r]);
-                sum[r] += x[r];
             }
             if (!ready) ok = ok && mbar_wait(p_empty, (t - 1) & 1);
             if (j0 + kTile > n && group == 0) {
@@ -421,23 +448,30 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
                                      "r"(0)
                                      : "memory");
             }
+            __syncwarp();
 #pragma unroll
-            for (int r = 0; r < RC; r += 8) {
-                uint32_t hi[4], lo[4];
+            for (int c = 0; c < RC; c += kPart) {
+                float x[kPart];
+                part_of(c, x, false);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float u = x[r + 2 * i], w = x[r + 2 * i + 1];
-                    hi[i] = Pair<T>::pack(u, w);
-                    const T* parts = reinterpret_cast<const T*>(&hi[i]);
-                    lo[i] = Pair<T>::pack(u - widen(parts[0]), w - widen(parts[1]));
+                for (int r = 0; r < kPart; ++r) {
+                    x[r] = ex2_ftz(x[r]);
+                    sum[c + r] += x[r];
                 }
-                const uint32_t to = p_at + ((c0 + r) >> 3) * 2048 + key * 16;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]),
-                             "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
-                             : "memory");
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + RT * 256),
-                             "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
-                             : "memory");
+#pragma unroll
+                for (int r = 0; r < kPart; r += 8) {
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        Pair<T>::split(x[r + 2 * i], x[r + 2 * i + 1], &hi[i], &lo[i]);
+                    const uint32_t to = p_at + ((c0 + c + r) >> 3) * 2048 + key * 16;
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]),
+                                 "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
+                                 : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + RT * 256),
+                                 "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
+                                 : "memory");
+                }
             }
             fence_async_smem();
             tc_fence_before();
@@ -446,7 +480,7 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
         join_lanes<RC>(sum, lane, [](float u, float w) { return u + w; });
         if (ok) ok = mbar_wait(p_empty, (tiles - 1) & 1);
         if (!ok) s_failed = 1;
-        red[quarter][c0 + own] = sum[0];
+        red[quarter][c0 + joined_at<RC>(lane)] = sum[0];
         softmax_sync<kSoftmax>();
         tc_fence_after();
         const int tid = threadIdx.x - 64;
@@ -459,14 +493,17 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
         }
         if (!s_failed)
             for (int m = 0; m * 128 < a.D; ++m) {
-                float o[RC];
-                tmem_ld<RC>(lanes + 2 * RT + m * RT, o);
                 const int d = m * 128 + key;
-                if (d < a.D) {
-                    float* to = part + ((bh * p.splits + split) * a.R + row0 + c0) * a.D + d;
+                float* to = part + ((bh * p.splits + split) * a.R + row0 + c0) * a.D + d;
+#pragma unroll 1
+                for (int c = 0; c < RC; c += kPart) {
+                    float o[kPart], lo[kPart];
+                    tmem_ld<kPart>(lanes + (2 + 2 * m) * RT + c, o);
+                    tmem_ld<kPart>(lanes + (3 + 2 * m) * RT + c, lo);
+                    if (d < a.D)
 #pragma unroll
-                    for (int r = 0; r < RC; ++r)
-                        if (c0 + r < rows) to[(int64_t)r * a.D] = o[r];
+                        for (int r = 0; r < kPart; ++r)
+                            if (c0 + c + r < rows) to[(int64_t)(c + r) * a.D] = o[r] + lo[r];
                 }
             }
         tc_fence_before();
@@ -649,6 +686,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         }
     } else if (warp == 1) {
         if (lane == 0) {
+            const uint64_t q_op = operand(q_at, 16, 1024, kSwizzle128);
             int item = 0, turns[2] = {0, 0};
             for (int64_t rg = rg0; rg < rgs && ok; ++rg) {
                 const int rows = (int)(a.R - rg * kScoreRows < kScoreRows ? a.R - rg * kScoreRows : kScoreRows);
@@ -661,13 +699,9 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                     if (!ok) break;
                     ++turns[half];
                     tc_fence_after();
-                    for (int kk = 0; kk * 16 < a.D; ++kk) {
-                        const uint32_t sub = kk >> 2, in = (kk & 3) * 32;
-                        mma_f16(tmem + half * kScoreRows,
-                                operand(ring + s * tile_bytes + sub * sub_bytes + in, 16, 1024, kSwizzle128),
-                                operand(q_at + sub * (kScoreRows * 128) + in, 16, 1024, kSwizzle128),
-                                shape, kk > 0);
-                    }
+                    key_products<kScoreRows>(tmem + half * kScoreRows,
+                                             operand(ring + s * tile_bytes, 16, 1024, kSwizzle128),
+                                             q_op, a.D, shape);
                     mma_commit(empty + 8 * s);
                     mma_commit(done + 8 * half);
                 }
@@ -745,24 +779,24 @@ bool attend_sizes_ok(int64_t B, int64_t Sq, int64_t Hq, int64_t Hkv, int64_t N, 
 AttendPlan make_plan(int64_t B, int64_t Sq, int64_t Hq, int64_t Hkv, int64_t N, int64_t D) {
     AttendPlan p{};
     const int64_t R = Sq * (Hq / Hkv), bh = B * Hkv;
-    p.rt = R <= 16 ? 16 : R <= 32 ? 32 : 64;
+    p.rt = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 || D > 128 ? 64 : 128;
     p.row_tiles = (int)((R + p.rt - 1) / p.rt);
     p.keep = R <= kKeepRows;
-    p.cols = 4 * p.rt;  // two tiles of logits, outputs of up to 256 columns
+    p.cols = D <= 128 ? 4 * p.rt : 8 * p.rt;  // logits of two tiles, and the outputs
     const int subs = (int)(D + 63) / 64, stage = subs * kTile * 128;
     // V^T is read 128 rows at a time: past an odd last block of 64 columns its (unused) rows
     // are whatever follows, which has to be there
     const int fixed = 1024 + subs * p.rt * 128 + p.rt * 512 + (subs % 2 ? kTile * 128 : 0);
     // two blocks an SM where three stages fit half of it
     const bool two = fixed + 3 * stage <= 112 * 1024;
-    const int room = (two ? 112 : 224) * 1024 - fixed;
+    const int room = (two ? 112 : kBlockSmem) * 1024 - fixed;
     p.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
     p.smem = fixed + p.stages * stage;
-    // Runs: enough blocks for every slot of 148 SMs, and with many heads runs of at most
-    // kRunTiles tiles, so that the last blocks to start are short
+    // Runs: one wave of blocks where the heads are few (less than half the slots); else
+    // runs of at most kRunTiles tiles, so that the last blocks to start are short
     const int64_t tiles = (N + kTile - 1) / kTile, slots = 148 * (two ? 2 : 1);
-    int64_t splits = (slots + bh * p.row_tiles - 1) / (bh * p.row_tiles);
-    if (splits < (tiles + kRunTiles - 1) / kRunTiles) splits = (tiles + kRunTiles - 1) / kRunTiles;
+    int64_t splits = slots / (bh * p.row_tiles);
+    if (splits < 2) splits = (tiles + kRunTiles - 1) / kRunTiles;
     p.splits = (int)(splits < tiles ? splits : tiles);
     p.RP = (R + 3) / 4 * 4;
     p.off_lse = up256((size_t)(bh * p.splits * R) * 8);
@@ -777,7 +811,7 @@ ScorePlan make_score_plan(int64_t bh, int64_t N, int64_t D) {
     const int subs = (int)(D + 63) / 64, tile = subs * kTile * 128, fixed = 1024 + subs * kScoreRows * 128;
     // two blocks an SM where two stages fit half of it
     const bool two = fixed + 2 * tile <= 112 * 1024;
-    const int room = (two ? 112 : 224) * 1024 - fixed;
+    const int room = (two ? 112 : kBlockSmem) * 1024 - fixed;
     p.stages = room / tile < kMaxStages ? room / tile : kMaxStages;
     p.smem = fixed + p.stages * tile;
     const int64_t tiles = (N + kTile - 1) / kTile, slots = 148 * (two ? 2 : 1);
@@ -837,7 +871,7 @@ cudaError_t launch_split(const AttendArgs& a, const AttendPlan& p, const void* q
     static std::atomic<unsigned long long> done{0};
     once_per_device(done, [] {
         cudaFuncSetAttribute(attend_split_kernel<T, RT, CW>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, 224 * 1024);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBlockSmem * 1024);
     });
     const int64_t blocks = (int64_t)a.B * a.Hkv * p.splits * p.row_tiles;
     return launch_pdl(attend_split_kernel<T, RT, CW>, dim3((unsigned)blocks), dim3(64 + 128 * CW),
@@ -857,7 +891,8 @@ cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& p, const void* 
         ProfScope prof("attend_split", st);
         e = p.rt == 16   ? launch_split<T, 16, 1>(a, p, q, k, v, stats, part, logits, st)
             : p.rt == 32 ? launch_split<T, 32, 2>(a, p, q, k, v, stats, part, logits, st)
-                         : launch_split<T, 64, 2>(a, p, q, k, v, stats, part, logits, st);
+            : p.rt == 64 ? launch_split<T, 64, 2>(a, p, q, k, v, stats, part, logits, st)
+                         : launch_split<T, 128, 4>(a, p, q, k, v, stats, part, logits, st);
     }
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.B * a.Hkv * a.R;
@@ -875,7 +910,7 @@ cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& p, const void* 
     static std::atomic<unsigned long long> done{0};
     once_per_device(done, [] {
         cudaFuncSetAttribute(attend_score_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             224 * 1024);
+                             kBlockSmem * 1024);
     });
     const ScorePlan sp = make_score_plan((int64_t)a.B * a.Hkv, a.N, a.D);
     return launch_pdl(attend_score_kernel<T>, dim3((unsigned)((int64_t)a.B * a.Hkv * sp.blocks)),

@@ -127,23 +127,6 @@ __device__ __forceinline__ void tmem_st<16>(uint32_t addr, const float (&v)[16])
           "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
         : "memory");
 }
-template <>
-__device__ __forceinline__ void tmem_st<32>(uint32_t addr, const float (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {"
-        "%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
-        "tcgen05.wait::st.sync.aligned;" ::"r"(addr),
-          "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
-          "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
-          "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
-          "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15])),
-          "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])), "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])),
-          "r"(__float_as_uint(v[20])), "r"(__float_as_uint(v[21])), "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])),
-          "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])), "r"(__float_as_uint(v[26])), "r"(__float_as_uint(v[27])),
-          "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])), "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
-        : "memory");
-}
 
 // --- matrix instruction --------------------------------------------------------------
 // Shared-memory operand descriptor.  Offsets in bytes, multiples of 16.
@@ -159,6 +142,8 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32
     return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)((lead >> 4) & 0x3fff) << 16) |
            ((uint64_t)((stride >> 4) & 0x3fff) << 32) | (1ull << 46) | layout;
 }
+// What to add to a descriptor to move its operand on by `bytes`.
+__device__ __forceinline__ constexpr uint64_t advance(uint32_t bytes) { return bytes >> 4; }
 // Instruction descriptor: fp32 accumulator, A and B both bf16 or both fp16, M x N.
 __device__ __forceinline__ uint32_t mma_shape(bool bf16, bool a_mn, bool b_mn, int m, int n) {
     const uint32_t t = bf16 ? 1u : 0u;
