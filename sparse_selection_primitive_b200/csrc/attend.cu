@@ -32,7 +32,7 @@ constexpr int kKeepRows = 16;       // logits of more rows a key are formed agai
 constexpr int kMaxStages = 6;
 constexpr int kRunTiles = 16;
 constexpr int kBlockSmem = 223;     // KB of dynamic shared memory of a block that has an SM to itself
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kJoinKeys = 512;
 
 struct AttendArgs {
     int64_t qb, qh, qr;  // element strides of q: batch, head, token
@@ -539,8 +539,51 @@ __device__ __forceinline__ float row_lse(const float2* stats, int splits, int64_
     return l > 0.f ? all + log2f(l) : INFINITY;
 }
 
-// Joins the runs.  The first blocks turn kept logits into scores, one thread a key; the
-// others join the outputs, one warp a row, and leave each row's log of the sum.
+// Scores of the kJoinKeys keys from j0 on out of kept logits, W float4 of rows a key (a
+// row that does not see a key has left -inf).  The logits are fetched before the rows'
+// logs are known.
+template <int W>
+__device__ __forceinline__ void kept_scores(const AttendArgs& a, const AttendPlan& p, int64_t bh,
+                                            int64_t b, int64_t h, int64_t j0, int64_t n,
+                                            const float2* stats, const float* logits,
+                                            const float* score_in, float* score_out, float* lse) {
+    constexpr int kOwn = kJoinKeys / kJoinThreads;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float4 x[kOwn][W];
+    float old[kOwn];
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        const int64_t j = j0 + i * kJoinThreads + threadIdx.x;
+        old[i] = 0.f;
+        if (j >= n) continue;
+        const float4* at = reinterpret_cast<const float4*>(logits + (bh * a.N + j) * (4 * W));
+#pragma unroll
+        for (int w = 0; w < W; ++w) x[i][w] = at[w];
+        if (score_in != nullptr) old[i] = score_in[b * a.sib + h * a.sih + j];
+    }
+    for (int r = warp; r < 4 * W; r += kJoinThreads / 32) {
+        const float v = r < a.R ? row_lse(stats + bh * p.splits * a.R + r, p.splits, a.R, lane)
+                                : INFINITY;
+        if (lane == 0) lse[r] = v;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        const int64_t j = j0 + i * kJoinThreads + threadIdx.x;
+        if (j >= n) continue;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float4 m = *reinterpret_cast<const float4*>(lse + 4 * w);
+            s += ex2_ftz(x[i][w].x - m.x) + ex2_ftz(x[i][w].y - m.y);
+            s += ex2_ftz(x[i][w].z - m.z) + ex2_ftz(x[i][w].w - m.w);
+        }
+        score_out[b * a.sob + h * a.soh + j] = old[i] + s;
+    }
+}
+
+// Joins the runs.  The first blocks turn kept logits into scores; the others join the
+// outputs, one warp a row, and leave each row's log of the sum.
 template <class T>
 __global__ void __launch_bounds__(kJoinThreads)
     attend_join_kernel(AttendArgs a, AttendPlan p, int64_t score_blocks, int key_blocks,
@@ -551,28 +594,14 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x < score_blocks) {
         const int64_t bh = blockIdx.x / key_blocks, b = bh / a.Hkv, h = bh - b * a.Hkv;
-        const int64_t n = cache_length(a, b);
-        const int64_t j0 = (int64_t)(blockIdx.x % key_blocks) * kJoinThreads, j = j0 + threadIdx.x;
+        const int64_t n = cache_length(a, b), j0 = (int64_t)(blockIdx.x % key_blocks) * kJoinKeys;
         if (j0 >= n) return;
-        for (int r = warp; r < p.RP; r += kJoinThreads / 32) {
-            const float v = r < a.R ? row_lse(stats + bh * p.splits * a.R + r, p.splits, a.R, lane)
-                                    : INFINITY;
-            if (lane == 0) lse[r] = v;
+        switch (p.RP / 4) {
+            case 1: kept_scores<1>(a, p, bh, b, h, j0, n, stats, logits, score_in, score_out, lse); break;
+            case 2: kept_scores<2>(a, p, bh, b, h, j0, n, stats, logits, score_in, score_out, lse); break;
+            case 3: kept_scores<3>(a, p, bh, b, h, j0, n, stats, logits, score_in, score_out, lse); break;
+            default: kept_scores<4>(a, p, bh, b, h, j0, n, stats, logits, score_in, score_out, lse);
         }
-        __syncthreads();
-        if (j >= n) return;
-        // rows from this one on see key j
-        const int64_t past = j - (n - a.Sq);
-        const float* x = logits + (bh * a.N + j) * p.RP;
-        float s = 0.f;
-        for (int r = (int)(past > 0 ? past * a.G : 0) & ~3; r < p.RP; r += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(x + r);
-            const float4 w = *reinterpret_cast<const float4*>(lse + r);
-            s += ex2_ftz(v.x - w.x) + ex2_ftz(v.y - w.y);
-            s += ex2_ftz(v.z - w.z) + ex2_ftz(v.w - w.w);
-        }
-        const float old = score_in != nullptr ? score_in[b * a.sib + h * a.sih + j] : 0.f;
-        score_out[b * a.sob + h * a.soh + j] = old + s;
         return;
     }
     const int64_t row = (blockIdx.x - score_blocks) * (kJoinThreads / 32) + warp;
@@ -622,7 +651,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 // two halves of the softmax warps take the tiles in turn, each with its own half of tensor
 // memory, and a thread sums one key's weights over the rows, whose logs it knows.
 template <class T>
-__global__ void __launch_bounds__(kScoreThreads, 1)
+__global__ void __launch_bounds__(kScoreThreads, 2)
     attend_score_kernel(AttendArgs a, ScorePlan p, const T* q,
                         const __grid_constant__ CUtensorMap k_map, const float* row_logs,
                         const float* score_in, float* score_out) {
@@ -898,7 +927,7 @@ cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& p, const void* 
     const int64_t rows = (int64_t)a.B * a.Hkv * a.R;
     {
         ProfScope prof("attend_join", st);
-        const int key_blocks = (int)((a.N + kJoinThreads - 1) / kJoinThreads);
+        const int key_blocks = (int)((a.N + kJoinKeys - 1) / kJoinKeys);
         const int64_t score_blocks = p.keep ? (int64_t)a.B * a.Hkv * key_blocks : 0;
         e = launch_pdl(attend_join_kernel<T>, dim3((unsigned)(score_blocks + (rows + 7) / 8)),
                        dim3(kJoinThreads), 0, st, a, p, score_blocks, key_blocks,
