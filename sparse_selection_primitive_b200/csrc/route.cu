@@ -74,6 +74,8 @@ __device__ __forceinline__ void load_lane(const T* row, int E, int lane, bool ve
     }
 }
 
+// 2^x by the hardware: off by two units, 0 below the smallest normal number
+__device__ __forceinline__ float exp2f_near(float x) { return ex2_ftz(x); }
 __device__ __forceinline__ float sigmoid_f(float l) { return 1.f / (1.f + expf(-l)); }
 
 // Where expert e of a row lies in the warp's scratch (padded against bank conflicts).
@@ -106,12 +108,11 @@ __device__ __forceinline__ F group_score(const F* keys, int size, int g, int gro
     return group_top == 2 && b > (F)-INFINITY ? a + b : a;
 }
 
-// The groups that are kept, as a bit mask: rank each group among all by (score,
-// lowest index).  `gap` (when not null) gets the distance between the last kept
-// and the first dropped score that are not both -inf.
+// Whether this lane's group g (value `mine`; `sub` lanes each) is among the `top` best
+// of all by (value, lowest index).  *gap gets the distance between the last kept and the
+// first dropped value (+inf where nothing is dropped).
 template <class F>
-__device__ __forceinline__ unsigned kept_groups(F mine, int g, int groups, int sub, int top,
-                                                F* gap) {
+__device__ __forceinline__ bool kept_here(F mine, int g, int groups, int sub, int top, F* gap) {
     int rank = 0;
     for (int o = 0; o < groups; ++o) {
         const F x = __shfl_sync(kAll, mine, o * sub);
@@ -119,19 +120,20 @@ __device__ __forceinline__ unsigned kept_groups(F mine, int g, int groups, int s
     }
     const bool real = g < groups && mine > (F)-INFINITY;
     const bool keep = real && rank < top;
-    unsigned mask = 0;
-    for (int o = 0; o < groups; ++o)
-        mask |= (__shfl_sync(kAll, keep ? 1u : 0u, o * sub)) << o;
-    if (gap != nullptr) {
-        F lo = keep ? mine : (F)INFINITY, hi = real && !keep ? mine : (F)-INFINITY;
+    F lo = keep ? mine : (F)INFINITY, hi = real && !keep ? mine : (F)-INFINITY;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) {
-            const F l2 = __shfl_xor_sync(kAll, lo, d), h2 = __shfl_xor_sync(kAll, hi, d);
-            lo = l2 < lo ? l2 : lo;
-            hi = h2 > hi ? h2 : hi;
-        }
-        *gap = hi > (F)-INFINITY && lo < (F)INFINITY ? lo - hi : (F)INFINITY;
+    for (int d = 16; d; d >>= 1) {
+        const F l2 = __shfl_xor_sync(kAll, lo, d), h2 = __shfl_xor_sync(kAll, hi, d);
+        lo = l2 < lo ? l2 : lo;
+        hi = h2 > hi ? h2 : hi;
     }
+    *gap = hi > (F)-INFINITY && lo < (F)INFINITY ? lo - hi : (F)INFINITY;
+    return keep;
+}
+__device__ __forceinline__ unsigned group_mask(bool keep, int groups, int sub) {
+    const unsigned lanes = __ballot_sync(kAll, keep);
+    unsigned mask = 0;
+    for (int o = 0; o < groups; ++o) mask |= ((lanes >> (o * sub)) & 1u) << o;
     return mask;
 }
 
@@ -166,7 +168,9 @@ __device__ __noinline__ int route_row_fp64(const T* row, const RouteArgs& a, int
         const int sub = 32 / gp, g = lane / sub;
         const double mine =
             group_score<double>(keys, size, g, a.groups, lane % sub, sub, a.group_top);
-        kept = kept_groups<double>(mine, g, a.groups, sub, a.top_groups, nullptr);
+        double gap;
+        kept = group_mask(kept_here<double>(mine, g, a.groups, sub, a.top_groups, &gap), a.groups,
+                          sub);
     }
     int chosen = -1;
     for (int j = 0; j < a.k; ++j) {
@@ -206,13 +210,93 @@ __device__ __noinline__ int route_row_fp64(const T* row, const RouteArgs& a, int
     return chosen;
 }
 
-// One warp per row.  kKeyed: keys are scores (+ bias) or groups limit the
-// choice; otherwise the logits are the keys.
+// Scores to within the bound below; __fdividef and ex2 are approximations of the hardware.
+__device__ __forceinline__ float near_sigmoid(float l) {
+    return __fdividef(1.f, 1.f + exp2f_near(-l * kLog2e));
+}
+
+// The `count` largest keys of a row in order, ties by the lower index: lane j gets the
+// j-th one's expert (-1: none) and key (0).  Every lane offers its largest key, and the
+// count-th largest offer bounds the answer from below; the keys that reach it, mostly
+// little more than `count`, are put side by side and ranked by counting.  Too many of them
+// (ties): the largest are taken out one by one.
+template <int V>
+__device__ __forceinline__ void take_largest(uint32_t (&key)[V], int count, int lane, uint2* cand,
+                                             int* chosen, uint32_t* chosen_key) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) best = max(best, key[i]);
+    uint32_t offer = best, bound = 1;
+    for (int j = 0; j < count; ++j) {
+        const uint32_t top = __reduce_max_sync(kAll, offer);
+        bound = top;
+        if (top == 0u) break;
+        if (offer == top) offer = 0;
+    }
+    bound = max(bound, 1u);
+    const unsigned below = (1u << lane) - 1u;
+    int found = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const bool in = key[i] >= bound;
+        const unsigned who = __ballot_sync(kAll, in);
+        const int at = found + __popc(who & below);
+        if (in && at < 32) cand[at] = make_uint2(key[i], (uint32_t)(lane * V + i));
+        found += __popc(who);
+    }
+    *chosen = -1;
+    *chosen_key = 0;
+    if (found <= 32) {
+        __syncwarp();
+        const uint2 mine = lane < found ? cand[lane] : make_uint2(0u, 0u);
+        int rank = 0;
+        for (int c = 0; c < found; ++c) {
+            const uint2 o = cand[c];
+            rank += (o.x > mine.x || (o.x == mine.x && o.y < mine.y)) ? 1 : 0;
+        }
+        __syncwarp();
+        if (lane < found) cand[rank] = mine;
+        __syncwarp();
+        if (lane < found && lane < count) {
+            *chosen = (int)cand[lane].y;
+            *chosen_key = cand[lane].x;
+        }
+        return;
+    }
+    for (int j = 0; j < count; ++j) {
+        const uint32_t top = __reduce_max_sync(kAll, best);
+        if (top == 0u) break;
+        const int src = __ffs(__ballot_sync(kAll, best == top)) - 1;
+        int at = 0;
+        if (lane == src) {
+            bool done = false;
+            best = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (!done && key[i] == top) {
+                    done = true;
+                    at = lane * V + i;
+                    key[i] = 0;
+                }
+                best = max(best, key[i]);
+            }
+        }
+        at = __shfl_sync(kAll, at, src);
+        if (lane == j) {
+            *chosen = at;
+            *chosen_key = top;
+        }
+    }
+}
+
+// One warp per row.  kKeyed: keys are scores (+ bias) or groups limit the choice;
+// otherwise the logits are the keys.
 template <class T, int V, bool kKeyed>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_kernel(const T* logits, RouteArgs a, float* weights, int32_t* experts) {
     pdl_wait();
     extern __shared__ double route_scratch[];
+    __shared__ uint2 candidates[kRouteWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp;
     if (t >= a.T) return;
@@ -220,20 +304,19 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     float l[V];
     load_lane<T, V>(row, a.E, lane, a.vec != 0, l);
 
-    float m = -INFINITY;
     bool bad = false;  // a NaN or +inf anywhere makes the row's answer NaN
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        bad |= !(l[i] < INFINITY);
-        m = fmaxf(m, l[i]);
-    }
-    m = warp_max(m);
+    for (int i = 0; i < V; ++i) bad |= !(l[i] < INFINITY);
 
-    float total = 0.f;  // softmax: the sum of e^{l - m} over all experts
+    float m = 0.f, total = 0.f;  // softmax: the largest logit, the sum of e^{l - m}
     if (!a.sigmoid && (kKeyed || !a.renorm)) {
+        m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+        m = warp_max(m);
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) s += l[i] == -INFINITY ? 0.f : expf(l[i] - m);
+        for (int i = 0; i < V; ++i) s += l[i] == -INFINITY ? 0.f : exp2f_near((l[i] - m) * kLog2e);
         total = warp_sum(s);
     }
 
@@ -250,39 +333,60 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
             const int e = lane * V + i;
             c[i] = -INFINITY;
             if (l[i] > -INFINITY) {
-                float x = a.sigmoid ? sigmoid_f(l[i]) : expf(l[i] - m) * inv;
+                float x = a.sigmoid ? near_sigmoid(l[i]) : exp2f_near((l[i] - m) * kLog2e) * inv;
                 if (a.bias != nullptr) x += a.bias[e];
                 bad |= !(x < INFINITY);
                 c[i] = x;
                 if (x > -INFINITY) cmax = fmaxf(cmax, fabsf(x));
             }
         }
-        // The scores' error is a few units of 2^-24 of the largest one (sigmoid:
-        // of 1; softmax: e^{l-m} carries |l - m| 2^-24 relative, and x e^{-x} < 1),
-        // the sum's 2^-24 of the key; 2^-20 of both together leaves room.
+        // How far a key may be off.  Sigmoid: e^-l is off by (|l| + 4) 2^-24 relative, which
+        // s (1 - s) brings below 1.3 units, the sum and the quotient by three more.  Softmax:
+        // 2 |l - m| + 4 units in the numerator, the same on average and V + 5 more in the
+        // sum, all relative to a score of at most 1 / sum.  The bias adds a rounding.
         cmax = warp_max(cmax);
-        tol = 9.5e-7f * (cmax + (a.sigmoid ? 1.f : inv));
-        unsigned kept = kAll;
+        tol = 5.97e-8f * ((a.sigmoid ? 8.f : 64.f * inv) + 2.f * cmax);
+        bool kept = true;           // this lane's experts are in a kept group
+        unsigned kept_mask = kAll;  // or which groups are
         const int size = a.E / a.groups;
+        // lanes per group, where its experts are whole lanes and a power of two of them
+        const int span = size % V == 0 && ((size / V) & (size / V - 1)) == 0 ? size / V : 0;
         if (a.groups > 1) {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (lane * V + i < a.E) fs[pad_slot(lane * V + i)] = c[i];
-            __syncwarp();
-            int gp = 1;
-            while (gp < a.groups) gp <<= 1;
-            const int sub = 32 / gp, g = lane / sub;
-            const float mine =
-                group_score<float>(fs, size, g, a.groups, lane % sub, sub, a.group_top);
             float gap;
-            kept = kept_groups<float>(mine, g, a.groups, sub, a.top_groups, &gap);
-            near |= gap <= 4.f * tol;
-            __syncwarp();
+            if (span > 0) {
+                float u = -INFINITY, w = -INFINITY;  // the group's two largest keys
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    w = fmaxf(w, fminf(u, c[i]));
+                    u = fmaxf(u, c[i]);
+                }
+                for (int d = 1; d < span; d <<= 1) {
+                    const float u2 = __shfl_xor_sync(kAll, u, d), w2 = __shfl_xor_sync(kAll, w, d);
+                    w = fmaxf(fminf(u, u2), fmaxf(w, w2));
+                    u = fmaxf(u, u2);
+                }
+                const float mine = a.group_top == 2 && w > -INFINITY ? u + w : u;
+                kept = kept_here<float>(mine, lane / span, a.groups, span, a.top_groups, &gap);
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (lane * V + i < a.E) fs[pad_slot(lane * V + i)] = c[i];
+                __syncwarp();
+                int gp = 1;
+                while (gp < a.groups) gp <<= 1;
+                const int sub = 32 / gp, g = lane / sub;
+                const float mine =
+                    group_score<float>(fs, size, g, a.groups, lane % sub, sub, a.group_top);
+                const bool keep = kept_here<float>(mine, g, a.groups, sub, a.top_groups, &gap);
+                kept_mask = group_mask(keep, a.groups, sub);
+                __syncwarp();
+            }
+            near |= gap <= 5.f * tol;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            const bool in = c[i] > -INFINITY && (a.groups == 1 || ((kept >> (e / size)) & 1u));
+            const bool in = c[i] > -INFINITY && kept &&
+                            (kept_mask == kAll || ((kept_mask >> ((lane * V + i) / size)) & 1u));
             // -0 and +0 are one value
             key[i] = in ? to_key((a.bias != nullptr ? c[i] : l[i]) + 0.f) : 0u;
         }
@@ -292,39 +396,19 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     }
     bad = __any_sync(kAll, bad);
 
-    uint32_t best = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) best = key[i] > best ? key[i] : best;
-    int chosen = -1;
-    uint32_t last = 0;
+    int chosen;
+    uint32_t mine;
     // with a bias one rank more is looked at: the chosen set ends between two keys
     const bool check = kKeyed && a.bias != nullptr;
-    const int rounds = a.k + (check ? 1 : 0);
-    for (int j = 0; j < rounds; ++j) {
-        const uint32_t top = __reduce_max_sync(kAll, best);
-        if (top == 0u) break;
+    take_largest<V>(key, a.k + (check && a.k < 32 ? 1 : 0), lane, candidates[warp], &chosen, &mine);
+    if constexpr (kKeyed) {
         if (check) {
-            near |= j > 0 && from_key(last) - from_key(top) <= 2.f * tol;
-            last = top;
+            const uint32_t next = __shfl_down_sync(kAll, mine, 1);
+            near |= lane < 31 && mine != 0u && next != 0u &&
+                    from_key(mine) - from_key(next) <= 2.f * tol;
+            near |= a.k == 32;  // no lane for the rank after the last
         }
-        const unsigned holders = __ballot_sync(kAll, best == top);
-        const int src = __ffs(holders) - 1;
-        int at = 0;
-        if (lane == src) {
-            bool found = false;
-            best = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                if (!found && key[i] == top) {
-                    found = true;
-                    at = lane * V + i;
-                    key[i] = 0;
-                }
-                best = key[i] > best ? key[i] : best;
-            }
-        }
-        at = __shfl_sync(kAll, at, src);
-        if (lane == j) chosen = at;  // the extra round's lane k keeps nothing: k < 32 or no lane
+        near = __any_sync(kAll, near);
     }
     if (lane >= a.k) chosen = -1;
     if constexpr (kKeyed) {
@@ -394,7 +478,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
             if (a.sigmoid) own *= sigmoid_f(-widen(row[e]));  // 1 - s
         }
     }
+    // every expert's gradient but for the chosen ones' own terms; those follow on top
     float d[V];
+    float base = 0.f;  // dense: the chosen expert's score
     if (dense) {
         float l[V];
         load_lane<T, V>(row, a.E, lane, a.vec != 0, l);
@@ -405,35 +491,18 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            l[i] = l[i] == -INFINITY ? 0.f : expf(l[i] - m);
-            s += l[i];
+            d[i] = l[i] == -INFINITY ? 0.f : exp2f_near((l[i] - m) * kLog2e);
+            s += d[i];
         }
         s = warp_sum(s);
         const float inv = s > 0.f ? 1.f / s : 0.f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = l[i] * inv;
-        float g[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) g[i] = -dot;
-        for (int j = 0; j < a.k; ++j) {
-            const int ej = __shfl_sync(kAll, e, j) - lane * V;
-            const float gj = __shfl_sync(kAll, own, j);
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (ej == i) g[i] += gj;
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = d[i] == 0.f ? 0.f : d[i] * g[i];
+        for (int i = 0; i < V; ++i) d[i] = d[i] == 0.f ? 0.f : d[i] * inv * -dot;
+        if (e >= 0) base = expf(widen(row[e]) - m) * inv;
+        own = base * (own - dot);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i) d[i] = 0.f;
-        for (int j = 0; j < a.k; ++j) {
-            const int ej = __shfl_sync(kAll, e, j) - lane * V;
-            const float gj = __shfl_sync(kAll, own, j);
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (ej == i) d[i] += gj;
-        }
     }
     if (bad) {
 #pragma unroll
@@ -441,20 +510,22 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     }
     constexpr int W = V * (int)sizeof(T) <= 16 ? V : 16 / (int)sizeof(T);
     T* o = out + t * ld_out;
-    const int base = lane * V;
+    const int first = lane * V;
 #pragma unroll
     for (int i = 0; i < V; i += W) {
-        if (vec_out && base + i + W <= a.E) {
+        if (vec_out && first + i + W <= a.E) {
             Pack<T, W> p;
 #pragma unroll
             for (int j = 0; j < W; ++j) p.v[j] = narrow<T>(d[i + j]);
-            *reinterpret_cast<Pack<T, W>*>(o + base + i) = p;
+            *reinterpret_cast<Pack<T, W>*>(o + first + i) = p;
         } else {
 #pragma unroll
             for (int j = 0; j < W; ++j)
-                if (base + i + j < a.E) o[base + i + j] = narrow<T>(d[i + j]);
+                if (first + i + j < a.E) o[first + i + j] = narrow<T>(d[i + j]);
         }
     }
+    __syncwarp();  // orders the row's stores before the chosen experts' own
+    if (e >= 0 && !bad) o[e] = narrow<T>(own);
 }
 
 int lane_values(int E) {
