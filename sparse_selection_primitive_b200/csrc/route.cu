@@ -137,28 +137,61 @@ __device__ __forceinline__ unsigned group_mask(bool keep, int groups, int sub) {
     return mask;
 }
 
+// What fp64 keys of a row take beside its own logit: nothing, or (softmax) the largest
+// logit and the sum of e^{l - m}.
+struct RowSum {
+    double m, total;
+};
+template <class T>
+__device__ __forceinline__ RowSum row_sum_fp64(const T* row, const RouteArgs& a, int lane) {
+    RowSum s{0.0, 1.0};
+    if (a.sigmoid) return s;
+    s.m = -INFINITY;
+    for (int e = lane; e < a.E; e += 32) s.m = fmax(s.m, (double)widen(row[e]));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s.m = fmax(s.m, __shfl_xor_sync(kAll, s.m, d));
+    s.total = 0.0;
+    for (int e = lane; e < a.E; e += 32) s.total += exp((double)widen(row[e]) - s.m);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s.total += __shfl_xor_sync(kAll, s.total, d);
+    return s;
+}
+template <class T>
+__device__ __forceinline__ double key_fp64(const T* row, const RouteArgs& a, int e, RowSum s) {
+    const double l = (double)widen(row[e]);
+    double c = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - s.m) / s.total;
+    if (a.bias != nullptr) c += (double)a.bias[e];
+    return l == -INFINITY ? -INFINITY : c;
+}
+
+// The order of `found` <= 32 candidates (lane c holds expert e) by their fp64 keys: the
+// j-th expert comes back on lane j.
+template <class T>
+__device__ __noinline__ int rank_fp64(const T* row, const RouteArgs& a, int lane, int e, int found) {
+    const RowSum s = row_sum_fp64(row, a, lane);
+    const double mine = lane < found ? key_fp64(row, a, e, s) : -INFINITY;
+    int rank = 0;
+    for (int c = 0; c < found; ++c) {
+        const double x = __shfl_sync(kAll, mine, c);
+        const int o = __shfl_sync(kAll, e, c);
+        rank += (x > mine || (x == mine && o < e)) ? 1 : 0;
+    }
+    int at = -1;
+    for (int c = 0; c < found; ++c) {
+        const int r = __shfl_sync(kAll, rank, c), o = __shfl_sync(kAll, e, c);
+        if (r == lane) at = o;
+    }
+    return at;
+}
+
 // The choice with fp64 keys, from the logits in memory: the j-th chosen expert
 // is returned on lane j (-1: none).  `keys` is the warp's scratch.
 template <class T>
 __device__ __noinline__ int route_row_fp64(const T* row, const RouteArgs& a, int lane,
                                            double* keys) {
-    double m = -INFINITY;
-    for (int e = lane; e < a.E; e += 32) m = fmax(m, (double)widen(row[e]));
-#pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmax(m, __shfl_xor_sync(kAll, m, d));
-    double total = 0.0;
-    if (!a.sigmoid) {
-        for (int e = lane; e < a.E; e += 32) total += exp((double)widen(row[e]) - m);
-#pragma unroll
-        for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(kAll, total, d);
-    }
+    const RowSum s = row_sum_fp64(row, a, lane);
     __syncwarp();
-    for (int e = lane; e < a.E; e += 32) {
-        const double l = (double)widen(row[e]);
-        double c = a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / total;
-        if (a.bias != nullptr) c += (double)a.bias[e];
-        keys[pad_slot(e)] = l == -INFINITY ? -INFINITY : c;
-    }
+    for (int e = lane; e < a.E; e += 32) keys[pad_slot(e)] = key_fp64(row, a, e, s);
     __syncwarp();
     unsigned kept = kAll;
     const int size = a.E / a.groups;
@@ -215,14 +248,15 @@ __device__ __forceinline__ float near_sigmoid(float l) {
     return __fdividef(1.f, 1.f + exp2f_near(-l * kLog2e));
 }
 
-// The `count` largest keys of a row in order, ties by the lower index: lane j gets the
-// j-th one's expert (-1: none) and key (0).  Every lane offers its largest key, and the
+// The largest keys of a row in order, ties by the lower index: lane j gets the j-th one's
+// expert (-1: none) and key (0), for `count` lanes at least.  Every lane offers its largest key, and the
 // count-th largest offer bounds the answer from below; the keys that reach it, mostly
 // little more than `count`, are put side by side and ranked by counting.  Too many of them
-// (ties): the largest are taken out one by one.
+// (ties): the largest are taken out one by one.  Returns how many lanes hold one when those
+// are all keys from *bound on, else 0.
 template <int V>
-__device__ __forceinline__ void take_largest(uint32_t (&key)[V], int count, int lane, uint2* cand,
-                                             int* chosen, uint32_t* chosen_key) {
+__device__ __forceinline__ int take_largest(uint32_t (&key)[V], int count, int lane, uint2* cand,
+                                            int* chosen, uint32_t* chosen_key, uint32_t* reach) {
     uint32_t best = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) best = max(best, key[i]);
@@ -257,11 +291,12 @@ __device__ __forceinline__ void take_largest(uint32_t (&key)[V], int count, int 
         __syncwarp();
         if (lane < found) cand[rank] = mine;
         __syncwarp();
-        if (lane < found && lane < count) {
+        if (lane < found) {
             *chosen = (int)cand[lane].y;
             *chosen_key = cand[lane].x;
         }
-        return;
+        *reach = bound;
+        return found;
     }
     for (int j = 0; j < count; ++j) {
         const uint32_t top = __reduce_max_sync(kAll, best);
@@ -287,6 +322,7 @@ __device__ __forceinline__ void take_largest(uint32_t (&key)[V], int count, int 
             *chosen_key = top;
         }
     }
+    return 0;
 }
 
 // One warp per row.  kKeyed: keys are scores (+ bias) or groups limit the choice;
@@ -397,24 +433,36 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     bad = __any_sync(kAll, bad);
 
     int chosen;
-    uint32_t mine;
-    // with a bias one rank more is looked at: the chosen set ends between two keys
+    uint32_t mine, reach = 0;
+    // with a bias more ranks are looked at: the chosen set ends between two keys
     const bool check = kKeyed && a.bias != nullptr;
-    take_largest<V>(key, a.k + (check && a.k < 32 ? 1 : 0), lane, candidates[warp], &chosen, &mine);
+    const int found = take_largest<V>(key, check ? min(a.k + 2, 32) : a.k, lane, candidates[warp],
+                                      &chosen, &mine, &reach);
     if constexpr (kKeyed) {
+        bool close = false;  // two neighbouring ranks that fp32 does not tell apart
         if (check) {
             const uint32_t next = __shfl_down_sync(kAll, mine, 1);
-            near |= lane < 31 && mine != 0u && next != 0u &&
-                    from_key(mine) - from_key(next) <= 2.f * tol;
-            near |= a.k == 32;  // no lane for the rank after the last
+            close = lane < a.k && (lane == 31 || (mine != 0u && next != 0u &&
+                                                  from_key(mine) - from_key(next) <= 2.f * tol));
+            close = __any_sync(kAll, close);
         }
-        near = __any_sync(kAll, near);
+        near = __any_sync(kAll, near);  // or two groups
+        if (close && !near && !bad) {
+            // all that may belong to the first k are among the candidates when those reach
+            // further than the error below the k-th
+            const uint32_t kth = __shfl_sync(kAll, mine, a.k - 1);
+            if (found > 0 && a.k < 32 && (kth == 0u || reach <= 1u ||
+                                          from_key(kth) - 2.f * tol > from_key(reach)))
+                chosen = rank_fp64<T>(row, a, lane, chosen, found);
+            else
+                near = true;
+        }
     }
-    if (lane >= a.k) chosen = -1;
     if constexpr (kKeyed) {
         if (near && !bad)
             chosen = route_row_fp64<T>(row, a, lane, route_scratch + (size_t)warp * a.scratch);
     }
+    if (lane >= a.k) chosen = -1;
 
     // weights: lane j owns the j-th choice
     float w = 0.f;
