@@ -8,6 +8,7 @@
 // read once and written to its k places, and a row of the result is summed from
 // its k places in the order j = 0 .. k - 1, so nothing depends on the order in
 // which blocks run.
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -19,10 +20,11 @@ namespace lapsum {
 namespace {
 
 constexpr int kPlanMaxE = 1024;
-constexpr int kPlanThreads = 256;
+constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanChunk = 2048;  // assignments per block
-constexpr int kWarpItems = kPlanChunk / kPlanWarps;
+constexpr int kPlanRounds = 8;                             // of 32 assignments a warp
+constexpr int kPlanChunk = kPlanThreads * kPlanRounds;     // assignments per block
+constexpr int kPlanFew = 64;  // chunks whose counts every block adds up by itself
 constexpr int kExpertMaxK = 32;
 constexpr unsigned kAll = 0xffffffffu;
 
@@ -49,6 +51,32 @@ __global__ void __launch_bounds__(kPlanThreads)
         counts[(int64_t)blockIdx.x * (E + 1) + e] = plan_smem[e];
 }
 
+// Many chunks: their counts become each bucket's total of the lower chunks, and the
+// totals follow as one more row.  A block takes 32 buckets, a warp 1/32 of the chunks.
+__global__ void __launch_bounds__(1024)
+    plan_scan_kernel(int32_t* counts, int chunks, int buckets) {
+    pdl_wait();
+    __shared__ int sums[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e = blockIdx.x * 32 + lane, per = (chunks + 31) / 32;
+    const int c0 = warp * per, c1 = c0 + per < chunks ? c0 + per : chunks;
+    int sum = 0;
+    if (e < buckets)
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c) sum += counts[(int64_t)c * buckets + e];
+    sums[warp][lane] = sum;
+    __syncthreads();
+    int at = 0;
+    for (int w = 0; w < warp; ++w) at += sums[w][lane];
+    if (e >= buckets) return;
+    if (warp == 31) counts[(int64_t)chunks * buckets + e] = at + sum;
+    for (int c = c0; c < c1; ++c) {
+        const int n = counts[(int64_t)c * buckets + e];
+        counts[(int64_t)c * buckets + e] = at;
+        at += n;
+    }
+}
+
 // Places of one chunk's assignments.  A bucket's first place in this chunk is the
 // total of the lower buckets plus this bucket's counts in the lower chunks;
 // inside the chunk the warps own consecutive runs of assignments and each warp
@@ -59,42 +87,53 @@ __global__ void __launch_bounds__(kPlanThreads)
     pdl_wait();
     extern __shared__ int plan_smem[];
     const int buckets = E + 1;
-    int* first = plan_smem;                // [buckets] this chunk's first place
-    int* warp_at = plan_smem + buckets;    // [warps][buckets] the warps' next places
+    int* total = plan_smem;                  // [buckets] over all chunks
+    int* lower = plan_smem + buckets;        // [buckets] over the lower ones
+    int* warp_at = plan_smem + 2 * buckets;  // [warps][buckets] the warps' next places
     __shared__ int warp_total[kPlanWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // a short chunk is shared out evenly too
+    const int64_t start = (int64_t)blockIdx.x * kPlanChunk;
+    const int here = (int)(N - start < kPlanChunk ? N - start : kPlanChunk);
+    const int rounds = (here + kPlanThreads - 1) / kPlanThreads;
+    const int64_t base = start + warp * (rounds * 32);
+    int mine[kPlanRounds];
+#pragma unroll
+    for (int i = 0; i < kPlanRounds; ++i) {
+        const int64_t at = base + i * 32 + lane;
+        mine[i] = i < rounds && at < N ? bucket(experts, at, E) : -1;
+    }
     for (int i = threadIdx.x; i < kPlanWarps * buckets; i += kPlanThreads) warp_at[i] = 0;
     __syncthreads();
-    const int64_t base = (int64_t)blockIdx.x * kPlanChunk + warp * kWarpItems;
-    int mine[kWarpItems / 32];
 #pragma unroll
-    for (int i = 0; i < kWarpItems / 32; ++i) {
-        const int64_t at = base + i * 32 + lane;
-        mine[i] = at < N ? bucket(experts, at, E) : -1;
+    for (int i = 0; i < kPlanRounds; ++i)
         if (mine[i] >= 0) atomicAdd(&warp_at[warp * buckets + mine[i]], 1);
-    }
-    __syncthreads();
-    // totals over all chunks and over the lower ones; each thread owns a run of buckets
-    const int per = (buckets + kPlanThreads - 1) / kPlanThreads;
-    int run = 0;
-    for (int i = 0; i < per; ++i) {
-        const int e = threadIdx.x * per + i;
-        if (e >= buckets) break;
-        int total = 0, lower = 0;
+    if (chunks == 1) __syncthreads();
+    for (int e = threadIdx.x; e < buckets; e += kPlanThreads) {
+        int all = 0, low = 0;
         if (chunks == 1) {
-            for (int w = 0; w < kPlanWarps; ++w) total += warp_at[w * buckets + e];
-        } else {
+#pragma unroll
+            for (int w = 0; w < kPlanWarps; ++w) all += warp_at[w * buckets + e];
+        } else if (chunks <= kPlanFew) {
+#pragma unroll 8
             for (int c = 0; c < chunks; ++c) {
                 const int n = counts[(int64_t)c * buckets + e];
-                total += n;
-                lower += c < (int)blockIdx.x ? n : 0;
+                all += n;
+                low += c < (int)blockIdx.x ? n : 0;
             }
+        } else {
+            all = counts[(int64_t)chunks * buckets + e];
+            low = counts[(int64_t)blockIdx.x * buckets + e];
         }
-        first[e] = run + lower;
-        if (offsets != nullptr && blockIdx.x == 0) offsets[e] = run;
-        run += total;
+        total[e] = all;
+        lower[e] = low;
     }
-    // exclusive scan of the threads' runs
+    __syncthreads();
+    // exclusive scan of the totals; each thread owns a run of buckets
+    const int per = (buckets + kPlanThreads - 1) / kPlanThreads;
+    const int e0 = threadIdx.x * per, e1 = e0 + per < buckets ? e0 + per : buckets;
+    int run = 0;
+    for (int e = e0; e < e1; ++e) run += total[e];
     int inc = run;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -103,13 +142,13 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     if (lane == 31) warp_total[warp] = inc;
     __syncthreads();
-    int before = inc - run;
-    for (int w = 0; w < warp; ++w) before += warp_total[w];
-    for (int i = 0; i < per; ++i) {
-        const int e = threadIdx.x * per + i;
-        if (e >= buckets) break;
-        if (blockIdx.x == 0) offsets[e] += before;
-        int at = first[e] + before;
+    int first = inc - run;
+    for (int w = 0; w < warp; ++w) first += warp_total[w];
+    for (int e = e0; e < e1; ++e) {
+        if (blockIdx.x == 0) offsets[e] = first;
+        int at = first + lower[e];
+        first += total[e];
+#pragma unroll
         for (int w = 0; w < kPlanWarps; ++w) {
             const int n = warp_at[w * buckets + e];
             warp_at[w * buckets + e] = at;
@@ -118,7 +157,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWarpItems / 32; ++i) {
+    for (int i = 0; i < kPlanRounds; ++i) {
+        if (i >= rounds) break;
         const unsigned same = __match_any_sync(kAll, mine[i]);
         const int64_t at = base + i * 32 + lane;
         int place = 0;
@@ -271,7 +311,7 @@ using namespace lapsum;
 extern "C" size_t lapsum_expert_plan_workspace_bytes(int64_t N, int64_t E) {
     if (N < 1 || N >= (int64_t(1) << 31) || E < 1 || E > kPlanMaxE) return 0;
     const int64_t chunks = (N + kPlanChunk - 1) / kPlanChunk;
-    const size_t need = chunks > 1 ? (size_t)chunks * (size_t)(E + 1) * 4 : 0;
+    const size_t need = chunks > 1 ? (size_t)(chunks + 1) * (size_t)(E + 1) * 4 : 0;
     return (need + 255) / 256 * 256 + 256;
 }
 
@@ -296,10 +336,20 @@ extern "C" int lapsum_expert_plan(const int32_t* experts, int64_t N, int64_t E, 
                        experts, N, (int)E, counts);
         if (e != cudaSuccess) return LAPSUM_ECUDA;
     }
+    if (chunks > kPlanFew) {
+        const cudaError_t e = launch_pdl(plan_scan_kernel, dim3((unsigned)(E + 32) / 32), dim3(1024),
+                                         0, st, counts, chunks, (int)E + 1);
+        if (e != cudaSuccess) return LAPSUM_ECUDA;
+    }
+    static std::atomic<unsigned long long> done{0};
+    once_per_device(done, [] {
+        cudaFuncSetAttribute(plan_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (kPlanWarps + 2) * (kPlanMaxE + 1) * 4);
+    });
     const cudaError_t e = launch_pdl(
         plan_place_kernel, dim3(chunks), dim3(kPlanThreads),
-        (size_t)(kPlanWarps + 1) * (E + 1) * 4, st, experts, N, (int)E, counts, chunks, offsets,
-        slots, order);
+        (size_t)(kPlanWarps + 2) * (E + 1) * 4, st, experts, N, (int)E, (const int32_t*)counts, chunks,
+        offsets, slots, order);
     return e == cudaSuccess ? LAPSUM_OK : LAPSUM_ECUDA;
 }
 
