@@ -71,7 +71,7 @@ def _once(backward):
 
 def _route_grad(logits, weights, experts, dweights, score, renormalize, scale):
     T, E = logits.shape
-    out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    out = logits.new_empty((T, E))
     if T > 0:
         launch(_lib().lapsum_route_backward, logits.device, logits.data_ptr(),
                DTYPES[logits.dtype], _ld(logits), T, E, experts.shape[1], score, renormalize,
@@ -156,14 +156,13 @@ def expert_plan(experts: torch.Tensor, num_experts: int) -> ExpertPlan:
     if N == 0:
         return ExpertPlan(torch.zeros(E + 1, dtype=torch.int32, device=dev),
                           torch.empty_like(experts), experts.new_empty(0))
-    offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    slots = torch.empty_like(experts)
-    order = torch.empty(N, dtype=torch.int32, device=dev)
     nbytes = _lib().lapsum_expert_plan_workspace_bytes(N, E)
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    # one piece of memory: the workspace (whole int32, aligned as the piece is), then the plan
+    ws, offsets, order, slots = experts.new_empty(nbytes // 4 + E + 1 + 2 * N).split(
+        (nbytes // 4, E + 1, N, N))
     launch(_lib().lapsum_expert_plan, dev, experts.data_ptr(), N, E, offsets.data_ptr(),
            slots.data_ptr(), order.data_ptr(), ws.data_ptr(), nbytes)
-    return ExpertPlan(offsets, slots, order)
+    return ExpertPlan(offsets, slots.view(experts.shape), order)
 
 
 def _check_plan(plan: ExpertPlan, device):
@@ -175,7 +174,7 @@ def _check_plan(plan: ExpertPlan, device):
 
 def _gather(x, plan):
     (T, H), k = x.shape, plan.slots.shape[1]
-    xs = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+    xs = x.new_empty((T * k, H))
     if xs.numel() > 0:
         launch(_lib().lapsum_expert_gather, x.device, x.data_ptr(), DTYPES[x.dtype], _ld(x), T, k,
                H, plan.slots.data_ptr(), plan.live, xs.data_ptr())
@@ -184,7 +183,7 @@ def _gather(x, plan):
 
 def _combine(y, weights, plan):
     (T, k), H = plan.slots.shape, y.shape[1]
-    out = torch.empty((T, H), dtype=y.dtype, device=y.device)
+    out = y.new_empty((T, H))
     if y.numel() == 0:
         return out.zero_()
     launch(_lib().lapsum_expert_combine, y.device, y.data_ptr(), DTYPES[y.dtype], T, k, H,
