@@ -49,12 +49,15 @@ struct AttendPlan {
     int rt;         // rows per tile
     int row_tiles;
     int splits;     // runs of key tiles per row tile
-    int stages, cols, smem;
+    int stages, smem;
     int keep;       // the logits are kept for the scores
     int64_t RP;     // rows of logits per key, padded
     size_t off_lse, off_part, off_logits, bytes;
 };
 
+constexpr int kNarrowThreads = 64 + 128;  // the kernel for up to kKeepRows rows a key, and its
+constexpr int kNarrowCols = 128;          // columns of tensor memory: 6 x 16, up to a power of two
+constexpr int kWideThreads = 64 + 256;    // the kernel for more
 // The score pass over keys whose logits were not kept.
 constexpr int kScoreRows = 128, kScoreThreads = 64 + 256;
 struct ScorePlan {
@@ -176,33 +179,32 @@ struct Pair<__half> {
 
 // One run of key tiles for one tile of rows.  Writes the rows' references and sums
 // (stats), the unnormalised outputs (part) and, where they are kept, the logits, all in
-// fp32.  Warp 0 loads, warp 1 multiplies, and 4 CW warps do the softmax: a warp can read
-// one quarter of the lanes of tensor memory, and CW warps share the rows of a quarter.
+// fp32.  Warp 0 loads, warp 1 multiplies, and four warps do the softmax, each on the
+// quarter of the lanes of tensor memory that it can read.
 //
 // Weights are 2^(x - m) with a reference m per row that is the exact maximum of the first
 // tile and is raised only when some logit passes it by kSlack: a maximum over the keys is a
 // maximum across threads, dear to form for every tile, and any reference within a factor
 // 2^kSlack of it serves as well (p <= 2^kSlack stays far inside fp16, and relative errors
 // are the same).  Raising it rescales the sums and the outputs in tensor memory.
-template <class T, int RT, int CW>
-__global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
-    attend_split_kernel(AttendArgs a, AttendPlan p, const T* q,
+template <class T>
+__global__ void __launch_bounds__(kNarrowThreads, 2)
+    attend_narrow_kernel(AttendArgs a, AttendPlan p, const T* q,
                         const __grid_constant__ CUtensorMap k_map,
                         const __grid_constant__ CUtensorMap v_map, float2* stats, float* part,
                         float* logits) {
-    constexpr int RC = RT / CW;  // rows of a softmax warp
-    constexpr int kSoftmax = 128 * CW;
+    constexpr int RT = kKeepRows;
     constexpr float kSlack = 12.f;
     extern __shared__ char smem_raw[];
     __shared__ uint64_t bars[2 * kMaxStages + 4];
     __shared__ uint32_t s_tmem;
     __shared__ int s_failed;
     __shared__ float red[4][RT];
-    // per row: the reference (0 while no key was seen) and what raising it last time
-    // multiplied sums with; per group of rows: how far a logit may pass it
-    __shared__ alignas(16) float s_ref[RT], s_scale[RT];
+    // per row: the reference (0 while no key was seen), by how much it rose last and what that
+    // multiplied sums with; and how far a logit may pass it
+    __shared__ alignas(16) float s_ref[RT], s_up[RT], s_scale[RT];
     __shared__ bool s_seen[RT];
-    __shared__ float s_slack[CW];
+    __shared__ float s_slack;
     __shared__ alignas(16) int s_lim[RT];  // keys that each row sees, from the run's first
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rt = blockIdx.x % p.row_tiles;
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
         }
         mbar_init(s_done, 1);
         mbar_init(s_done + 8, 1);
-        mbar_init(p_full, kSoftmax);
+        mbar_init(p_full, 128);
         mbar_init(p_empty, 1);
         fence_barrier_init();
         s_failed = 0;
@@ -253,11 +255,11 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
         lim = lim < 0 ? 0 : lim;
         s_ref[threadIdx.x] = 0.f;
         s_seen[threadIdx.x] = false;
-        if (threadIdx.x < CW) s_slack[threadIdx.x] = -INFINITY;
+        if (threadIdx.x == 0) s_slack = -INFINITY;
         s_lim[threadIdx.x] = (int)(threadIdx.x < rows && lim < most ? lim : most);
     }
-    if (warp == 1) tmem_alloc(smem_addr(&s_tmem), p.cols);
-    load_rows<T, RT>(a, q, b, h, row0, rows, q_at, threadIdx.x, 64 + kSoftmax);
+    if (warp == 1) tmem_alloc(smem_addr(&s_tmem), kNarrowCols);
+    load_rows<T, RT>(a, q, b, h, row0, rows, q_at, threadIdx.x, kNarrowThreads);
     fence_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -330,158 +332,132 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
     } else {
         const int quarter = warp & 3;                  // the lanes of tensor memory it may read
         const int key = quarter * 32 + lane;           // of a tile
-        const int group = (warp - 2) / 4, c0 = group * RC;  // its first row
-        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
-        constexpr int kPart = RC < 16 ? RC : 16;       // rows in registers at a time
-        float sum[RC];
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const int own = joined_at<RT>(lane);
+        float sum[RT];
 #pragma unroll
-        for (int r = 0; r < RC; ++r) sum[r] = 0.f;
+        for (int r = 0; r < RT; ++r) sum[r] = 0.f;
         for (int t = 0; t < tiles; ++t) {
             ok = ok && mbar_wait(s_done + 8 * (t & 1), (t >> 1) & 1);
             ok = __all_sync(kAll, ok);
             tc_fence_after();
+            float x[RT];
+            tmem_ld<RT>(lanes + (t & 1) * RT, x);
             const int64_t j0 = (first + t) * kTile, j = j0 + key;
-            const bool whole = (t + 1) * kTile <= s_lim[0];  // the first row sees the fewest
-            // the logits of kPart rows from c on, less the rows' references where asked
-            const auto part_of = [&](int c, float (&x)[kPart], bool keep) {
-                tmem_ld<kPart>(lanes + (t & 1) * RT + c, x);
-                const int r0 = c0 + c;
-                if (RT == kKeepRows) {
 #pragma unroll
-                    for (int r = 0; r < kPart; ++r) x[r] *= a.scale_log2;
-                } else {
+            for (int r = 0; r < RT; ++r) x[r] *= a.scale_log2;
+            if ((t + 1) * kTile > s_lim[0]) {  // the first row sees the fewest
+                const int at = t * kTile + key;
 #pragma unroll
-                    for (int r = 0; r < kPart; ++r) x[r] = fmaf(x[r], a.scale_log2, -s_ref[r0 + r]);
-                }
-                if (!whole) {
-                    const int at = t * kTile + key;
+                for (int r = 0; r < RT; ++r)
+                    if (at >= s_lim[r]) x[r] = -INFINITY;
+            }
+            if (j < n) {
+                float* to = logits + (bh * a.N + j) * p.RP + row0;
 #pragma unroll
-                    for (int r = 0; r < kPart; ++r)
-                        if (at >= s_lim[r0 + r]) x[r] = -INFINITY;
-                }
-                if (RT == kKeepRows) {
-                    if (keep && j < n) {
-                        float* to = logits + (bh * a.N + j) * p.RP + row0 + r0;
-#pragma unroll
-                        for (int r = 0; r < kPart; r += 4)
-                            if (row0 + r0 + r < p.RP)
-                                *reinterpret_cast<float4*>(to + r) =
-                                    make_float4(x[r], x[r + 1], x[r + 2], x[r + 3]);
-                    }
-#pragma unroll
-                    for (int r = 0; r < kPart; ++r) x[r] -= s_ref[r0 + r];
-                }
-            };
+                for (int r = 0; r < RT; r += 4)
+                    if (row0 + r < p.RP)
+                        *reinterpret_cast<float4*>(to + r) =
+                            make_float4(x[r], x[r + 1], x[r + 2], x[r + 3]);
+            }
             float over[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < RC; c += kPart) {
-                float x[kPart];
-                part_of(c, x, true);
-#pragma unroll
-                for (int r = 0; r < kPart; ++r) over[r & 3] = fmaxf(over[r & 3], x[r]);
+            for (int r = 0; r < RT; ++r) {
+                x[r] -= s_ref[r];
+                over[r & 3] = fmaxf(over[r & 3], x[r]);
             }
-            const bool past = fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > s_slack[group];
-            // one answer for the four warps that share these rows
+            const bool past = fmaxf(fmaxf(over[0], over[1]), fmaxf(over[2], over[3])) > s_slack;
+            // one answer for the four warps
             uint32_t raise;
             asm volatile(
                 "{\n\t.reg .pred u, v;\n\tsetp.ne.u32 u, %1, 0;\n\t"
-                "barrier.cta.red.or.pred v, %2, 128, u;\n\tselp.u32 %0, 1, 0, v;\n\t}"
+                "barrier.cta.red.or.pred v, 2, 128, u;\n\tselp.u32 %0, 1, 0, v;\n\t}"
                 : "=r"(raise)
-                : "r"(past ? 1u : 0u), "r"(2 + group)
+                : "r"(past ? 1u : 0u)
                 : "memory");
             // the outputs so far are complete, and the weights' room is free
-            bool ready = t == 0;
+            ok = ok && (t == 0 || mbar_wait(p_empty, (t - 1) & 1));
+            ok = __all_sync(kAll, ok);
             if (raise) {
-                if (!ready) {
-                    ok = ok && mbar_wait(p_empty, (t - 1) & 1);
-                    ok = __all_sync(kAll, ok);
-                    tc_fence_after();
-                    ready = true;
+                tc_fence_after();
+                {
+                    float top[RT];
+#pragma unroll
+                    for (int r = 0; r < RT; ++r) top[r] = x[r];
+                    join_lanes<RT>(top, lane, [](float u, float w) { return fmaxf(u, w); });
+                    red[quarter][own] = top[0];
                 }
-#pragma unroll 1
-                for (int c = 0; c < RC; c += kPart) {
-                    float x[kPart];
-                    part_of(c, x, false);
-                    join_lanes<kPart>(x, lane, [](float u, float w) { return fmaxf(u, w); });
-                    red[quarter][c0 + c + joined_at<kPart>(lane)] = x[0];
-                }
-                asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
+                softmax_sync<128>();
                 if (key < 32) {
                     bool unseen = false;
-                    if (key < RC) {
-                        const int c = c0 + key;
-                        const float by = fmaxf(fmaxf(red[0][c], red[1][c]), fmaxf(red[2][c], red[3][c]));
-                        unseen = !s_seen[c] && by == -INFINITY;
-                        const float up = unseen ? 0.f : s_seen[c] ? fmaxf(by, 0.f) : by;
-                        s_ref[c] += up;
-                        s_scale[c] = s_seen[c] ? ex2_ftz(-up) : 0.f;
-                        s_seen[c] = !unseen;
+                    if (key < RT) {
+                        const float by = fmaxf(fmaxf(red[0][key], red[1][key]), fmaxf(red[2][key], red[3][key]));
+                        unseen = !s_seen[key] && by == -INFINITY;
+                        const float up = unseen ? 0.f : s_seen[key] ? fmaxf(by, 0.f) : by;
+                        s_ref[key] += up;
+                        s_up[key] = up;
+                        s_scale[key] = s_seen[key] ? ex2_ftz(-up) : 0.f;
+                        s_seen[key] = !unseen;
                     }
                     unseen = __any_sync(kAll, unseen);
-                    if (key == 0) s_slack[group] = unseen ? -INFINITY : kSlack;
+                    if (key == 0) s_slack = unseen ? -INFINITY : kSlack;
                 }
-                asm volatile("bar.sync %0, 128;" ::"r"(2 + group) : "memory");
+                softmax_sync<128>();
 #pragma unroll
-                for (int r = 0; r < RC; ++r) sum[r] *= s_scale[c0 + r];
-                if (t > 0)
-#pragma unroll 1
-                    for (int c = 0; c < (a.D + 127) / 128 * 2 * RC; c += kPart) {
-                        // hi and lo parts of the outputs, of the first and the second 128 columns
-                        const int at = c % RC;
-                        float o[kPart];
-                        tmem_ld<kPart>(lanes + 2 * RT + c / RC * RT + at, o);
+                for (int r = 0; r < RT; ++r) {
+                    x[r] -= s_up[r];
+                    sum[r] *= s_scale[r];
+                }
+                if (t > 0)  // hi and lo parts of the outputs, of the first and the second 128 columns
+                    for (int m = 0; m < (a.D + 127) / 128 * 2; ++m) {
+                        float o[RT];
+                        tmem_ld<RT>(lanes + (2 + m) * RT, o);
 #pragma unroll
-                        for (int r = 0; r < kPart; ++r) o[r] *= s_scale[c0 + at + r];
-                        tmem_st<kPart>(lanes + 2 * RT + c / RC * RT + at, o);
+                        for (int r = 0; r < RT; ++r) o[r] *= s_scale[r];
+                        tmem_st<RT>(lanes + (2 + m) * RT, o);
                     }
             }
-            if (!ready) ok = ok && mbar_wait(p_empty, (t - 1) & 1);
-            if (j0 + kTile > n && group == 0) {
+            if (j0 + kTile > n) {
                 // value rows behind the cache's end may hold anything: 0 x NaN is NaN
                 const int item = value_item(t), s = item % p.stages;
                 ok = ok && mbar_wait(full + 8 * s, (item / p.stages) & 1);
-                if (j >= n)
+                if (ok && j >= n)
                     for (int c = 0; c < subs * 8; ++c)
                         asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                                          ring + s * stage_bytes + (c >> 3) * sub_bytes + key * 128 +
                                          (c & 7) * 16),
                                      "r"(0)
                                      : "memory");
+                __syncwarp();
             }
-            __syncwarp();
 #pragma unroll
-            for (int c = 0; c < RC; c += kPart) {
-                float x[kPart];
-                part_of(c, x, false);
+            for (int r = 0; r < RT; ++r) {
+                x[r] = ex2_ftz(x[r]);
+                sum[r] += x[r];
+            }
 #pragma unroll
-                for (int r = 0; r < kPart; ++r) {
-                    x[r] = ex2_ftz(x[r]);
-                    sum[c + r] += x[r];
-                }
+            for (int r = 0; r < RT; r += 8) {
+                uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int r = 0; r < kPart; r += 8) {
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        Pair<T>::split(x[r + 2 * i], x[r + 2 * i + 1], &hi[i], &lo[i]);
-                    const uint32_t to = p_at + ((c0 + c + r) >> 3) * 2048 + key * 16;
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]),
-                                 "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
-                                 : "memory");
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + RT * 256),
-                                 "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
-                                 : "memory");
-                }
+                for (int i = 0; i < 4; ++i)
+                    Pair<T>::split(x[r + 2 * i], x[r + 2 * i + 1], &hi[i], &lo[i]);
+                const uint32_t to = p_at + (r >> 3) * 2048 + key * 16;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]),
+                             "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
+                             : "memory");
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + RT * 256),
+                             "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3])
+                             : "memory");
             }
             fence_async_smem();
             tc_fence_before();
             mbar_arrive(p_full);
         }
-        join_lanes<RC>(sum, lane, [](float u, float w) { return u + w; });
+        join_lanes<RT>(sum, lane, [](float u, float w) { return u + w; });
         if (ok) ok = mbar_wait(p_empty, (tiles - 1) & 1);
         if (!ok) s_failed = 1;
-        red[quarter][c0 + joined_at<RC>(lane)] = sum[0];
-        softmax_sync<kSoftmax>();
+        red[quarter][own] = sum[0];
+        softmax_sync<128>();
         tc_fence_after();
         const int tid = threadIdx.x - 64;
         if (tid < rows) {
@@ -494,17 +470,14 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
         if (!s_failed)
             for (int m = 0; m * 128 < a.D; ++m) {
                 const int d = m * 128 + key;
-                float* to = part + ((bh * p.splits + split) * a.R + row0 + c0) * a.D + d;
-#pragma unroll 1
-                for (int c = 0; c < RC; c += kPart) {
-                    float o[kPart], lo[kPart];
-                    tmem_ld<kPart>(lanes + (2 + 2 * m) * RT + c, o);
-                    tmem_ld<kPart>(lanes + (3 + 2 * m) * RT + c, lo);
-                    if (d < a.D)
+                float* to = part + ((bh * p.splits + split) * a.R + row0) * a.D + d;
+                float o[RT], lo[RT];
+                tmem_ld<RT>(lanes + (2 + 2 * m) * RT, o);
+                tmem_ld<RT>(lanes + (3 + 2 * m) * RT, lo);
+                if (d < a.D)
 #pragma unroll
-                        for (int r = 0; r < kPart; ++r)
-                            if (c0 + c + r < rows) to[(int64_t)(c + r) * a.D] = o[r] + lo[r];
-                }
+                    for (int r = 0; r < RT; ++r)
+                        if (r < rows) to[(int64_t)r * a.D] = o[r] + lo[r];
             }
         tc_fence_before();
     }
@@ -512,7 +485,275 @@ __global__ void __launch_bounds__(64 + 128 * CW, RT == 16 ? 2 : 1)
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_free(tmem, p.cols);
+        tmem_free(tmem, kNarrowCols);
+    }
+}
+
+// The same run for a tile of up to 128 rows, where rows fill the M side: S = Q K^T,
+// and a thread holds one row's logits of half a tile of keys, so that maxima and sums need no
+// exchange but that of two threads.  The weights go back into tensor memory, over the
+// logits they came from (hi and lo parts side by side), and are the A operand of O += P V there:
+// with them in shared memory its bandwidth was the limit (288 KB a tile and 128 rows, 2300 of
+// 4300 cycles).
+template <class T>
+__global__ void __launch_bounds__(kWideThreads, 1)
+    attend_wide_kernel(AttendArgs a, AttendPlan p, const T* q,
+                       const __grid_constant__ CUtensorMap k_map,
+                       const __grid_constant__ CUtensorMap v_map, float2* stats, float* part) {
+    constexpr int RT = 128, kHalf = kTile / 2;
+    constexpr float kSlack = 12.f;
+    extern __shared__ char smem_raw[];
+    __shared__ uint64_t bars[2 * kMaxStages + 5];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_failed;
+    __shared__ float s_pair[2][RT];  // what the two threads of a row tell each other
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rt = blockIdx.x % p.row_tiles;
+    const int64_t rest = blockIdx.x / p.row_tiles;
+    const int split = (int)(rest % p.splits);
+    const int64_t bh = rest / p.splits;
+    const int b = (int)(bh / a.Hkv), h = (int)(bh % a.Hkv);
+    const int64_t row0 = (int64_t)rt * RT;
+    const int rows = (int)(a.R - row0 < RT ? a.R - row0 : RT);
+    float2* my_stats = stats + (bh * p.splits + split) * a.R + row0;
+
+    pdl_wait();
+    const int64_t n = cache_length(a, b);
+    // keys that the tile's last row sees, and this run's tiles among them
+    int64_t seen = n - a.Sq + 1 + (row0 + rows - 1) / a.G;
+    seen = seen < 0 ? 0 : seen;
+    const int64_t all_tiles = (seen + kTile - 1) / kTile;
+    const int64_t per = (all_tiles + p.splits - 1) / p.splits;
+    const int64_t first = split * per;
+    const int tiles = (int)(all_tiles - first < per ? all_tiles - first : per);
+    if (tiles <= 0) {
+        if (threadIdx.x < rows) my_stats[threadIdx.x] = make_float2(-INFINITY, 0.f);
+        return;
+    }
+
+    const int subs = (a.D + 63) / 64;
+    const uint32_t sub_bytes = kTile * 128, stage_bytes = subs * sub_bytes;
+    const uint32_t ring = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t q_at = ring + p.stages * stage_bytes;
+    const uint32_t full = smem_addr(bars), empty = full + 8 * kMaxStages,
+                   s_done = empty + 8 * kMaxStages, p_full = s_done + 16, p_used = p_full + 16;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        mbar_init(s_done, 1);
+        mbar_init(s_done + 8, 1);
+        mbar_init(p_full, 256);  // one per half: the softmax may be a tile ahead of the product
+        mbar_init(p_full + 8, 256);
+        mbar_init(p_used, 1);
+        fence_barrier_init();
+        s_failed = 0;
+    }
+    if (warp == 1) tmem_alloc(smem_addr(&s_tmem), 512);
+    load_rows<T, RT>(a, q, b, h, row0, rows, q_at, threadIdx.x, kWideThreads);
+    fence_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // logits (then weights) of two tiles, then the outputs
+    const uint32_t tmem = s_tmem, o_col = tmem + 2 * kTile;
+    // the ring's items: K0, K1, V0, K2, V1, ..., V(last)
+    const int items = 2 * tiles;
+    auto key_item = [](int t) { return t == 0 ? 0 : 2 * t - 1; };
+    auto value_item = [&](int t) { return t + 1 < tiles ? 2 * t + 2 : 2 * t + 1; };
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int issued = 0;
+            for (; issued < items; ++issued) {
+                const int s = issued % p.stages, turn = issued / p.stages;
+                if (turn > 0) ok = mbar_wait(empty + 8 * s, (turn - 1) & 1);
+                if (!ok) break;
+                mbar_expect(full + 8 * s, stage_bytes);
+                const bool key = issued == 0 || (issued % 2 == 1 && issued < items - 1);
+                const int t = key ? (issued + 1) / 2 : (issued - 1) / 2;
+                const int y = (int)((first + t) * kTile);
+                for (int c = 0; c < subs; ++c)
+                    tma_load_4d(ring + s * stage_bytes + c * sub_bytes, key ? &k_map : &v_map,
+                                full + 8 * s, c * 64, y, h * (key ? a.kh : a.vh),
+                                b * (key ? a.kb : a.vb));
+            }
+            if (!ok)  // gave up: let the copies in flight land before the block ends
+                for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+                    mbar_wait(full + 8 * (i % p.stages), (i / p.stages) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t shape_s = mma_shape(Pair<T>::bf16, false, false, RT, kTile);
+            const uint32_t shape_o = mma_shape(Pair<T>::bf16, false, true, RT, a.D);
+            const uint64_t q_op = operand(q_at, 16, 1024, kSwizzle128);
+            auto logits_of = [&](int t) {  // S of tile t into its half
+                const int item = key_item(t), s = item % p.stages;
+                if (!mbar_wait(full + 8 * s, (item / p.stages) & 1)) return false;
+                tc_fence_after();
+                key_products<RT>(tmem + (t & 1) * kTile, q_op,
+                                 operand(ring + s * stage_bytes, 16, 1024, kSwizzle128), a.D, shape_s);
+                mma_commit(empty + 8 * s);
+                mma_commit(s_done + 8 * (t & 1));
+                return true;
+            };
+            ok = logits_of(0) && (tiles == 1 || logits_of(1));
+            for (int t = 0; t < tiles && ok; ++t) {
+                const int item = value_item(t), s = item % p.stages;
+                ok = mbar_wait(full + 8 * s, (item / p.stages) & 1) && mbar_wait(p_full + 8 * (t & 1), (t >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                // 16 keys at a time: 8 columns of weights; each half of the tile has its hi
+                // parts in 32 columns and its lo parts in the next 32
+                const uint64_t v = operand(ring + s * stage_bytes, sub_bytes, 1024, kSwizzle128);
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk) {
+                    const uint32_t w = tmem + (t & 1) * kTile + (kk >> 2) * kHalf + (kk & 3) * 8;
+                    mma_f16_ta(o_col, w, v + advance(kk * 2048), shape_o, t + kk > 0);
+                    mma_f16_ta(o_col, w + 32, v + advance(kk * 2048), shape_o, true);
+                }
+                mma_commit(empty + 8 * s);
+                mma_commit(p_used);
+                // the next logits of this half go over weights that the product has read
+                if (t + 2 < tiles) ok = mbar_wait(p_used, t & 1) && logits_of(t + 2);
+            }
+        }
+    } else {
+        const int quarter = warp & 3, half = (warp - 2) / 4;
+        const int row = quarter * 32 + lane;  // of the tile
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const bool busy = quarter * 32 < rows;  // warps without a row only keep step
+        // keys that the row sees, and the fewest that any row does, from the run's first
+        const int64_t most = (int64_t)tiles * kTile;
+        int64_t lim64 = n - a.Sq + 1 + (row0 + row) / a.G - first * kTile;
+        const int lim = (int)(row >= rows || lim64 > most ? most : lim64 < 0 ? 0 : lim64);
+        lim64 = n - a.Sq + 1 + row0 / a.G - first * kTile;
+        const int least = (int)(lim64 > most ? most : lim64 < 0 ? 0 : lim64);
+        float ref = 0.f, sum = 0.f;
+        bool fresh = true;  // the row has seen no key yet
+        for (int t = 0; t < tiles; ++t) {
+            ok = ok && mbar_wait(s_done + 8 * (t & 1), (t >> 1) & 1);
+            ok = __all_sync(kAll, ok);
+            tc_fence_after();
+            const uint32_t at = lanes + (t & 1) * kTile + half * kHalf;
+            const int key0 = t * kTile + half * kHalf;
+            const int64_t j0 = (first + t) * kTile;
+            if (j0 + kTile > n && half == 0) {
+                // value rows behind the cache's end may hold anything: 0 x NaN is NaN
+                const int item = value_item(t), s = item % p.stages;
+                ok = ok && mbar_wait(full + 8 * s, (item / p.stages) & 1);
+                if (ok && j0 + row >= n)
+                    for (int c = 0; c < subs * 8; ++c)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         ring + s * stage_bytes + (c >> 3) * sub_bytes + row * 128 +
+                                         (c & 7) * 16),
+                                     "r"(0)
+                                     : "memory");
+                fence_async_smem();
+                __syncwarp();
+            }
+            if (busy) {
+                float x[kHalf];
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 32)
+                    tmem_ld<32>(at + c, *reinterpret_cast<float(*)[32]>(x + c));
+#pragma unroll
+                for (int c = 0; c < kHalf; ++c) x[c] = fmaf(x[c], a.scale_log2, -ref);
+                if (key0 + kHalf > least)
+#pragma unroll
+                    for (int c = 0; c < kHalf; ++c)
+                        if (key0 + c >= lim) x[c] = -INFINITY;
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < kHalf; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
+                const float by = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                // one answer for the two warps that share these rows
+                uint32_t raise;
+                asm volatile(
+                    "{\n\t.reg .pred u, v;\n\tsetp.ne.u32 u, %1, 0;\n\t"
+                    "barrier.cta.red.or.pred v, %2, 64, u;\n\tselp.u32 %0, 1, 0, v;\n\t}"
+                    : "=r"(raise)
+                    : "r"(by > (fresh ? -INFINITY : kSlack) ? 1u : 0u), "r"(2 + quarter)
+                    : "memory");
+                if (raise) {
+                    s_pair[half][row] = by;
+                    if (t > 0) {  // the outputs so far are complete
+                        ok = ok && mbar_wait(p_used, (t - 1) & 1);
+                        ok = __all_sync(kAll, ok);
+                        tc_fence_after();
+                    }
+                    asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory");
+                    const float both = fmaxf(s_pair[0][row], s_pair[1][row]);
+                    asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory");
+                    const bool none = fresh && both == -INFINITY;
+                    const float up = none ? 0.f : fresh ? both : fmaxf(both, 0.f);
+                    const float scale = fresh ? 0.f : ex2_ftz(-up);
+                    ref += up;
+                    fresh = none;
+                    sum *= scale;
+#pragma unroll
+                    for (int c = 0; c < kHalf; ++c) x[c] -= up;
+                    if (t > 0)  // each thread rescales half of the row's outputs
+                        for (int c = half * 16; c < a.D; c += 32) {
+                            float o[16];
+                            tmem_ld<16>(lanes + 2 * kTile + c, o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] *= scale;
+                            tmem_st<16>(lanes + 2 * kTile + c, o);
+                        }
+                }
+                float part_sum[4] = {0.f, 0.f, 0.f, 0.f};
+                uint32_t hi[kHalf / 2], lo[kHalf / 2];
+#pragma unroll
+                for (int c = 0; c < kHalf; c += 2) {
+                    const float u = ex2_ftz(x[c]), w = ex2_ftz(x[c + 1]);
+                    part_sum[c & 3] += u;
+                    part_sum[(c & 3) + 1] += w;
+                    Pair<T>::split(u, w, &hi[c / 2], &lo[c / 2]);
+                }
+                sum += (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
+                tmem_st<32>(at, hi);
+                tmem_st<32>(at + 32, lo);
+            }
+            tc_fence_before();
+            mbar_arrive(p_full + 8 * (t & 1));
+        }
+        // both products that may be under way: of a barrier two phases behind, the last one
+        // would look complete
+        if (ok && tiles > 1) ok = mbar_wait(p_used, (tiles - 2) & 1);
+        if (ok) ok = mbar_wait(p_used, (tiles - 1) & 1);
+        if (!ok) s_failed = 1;
+        s_pair[half][row] = sum;
+        softmax_sync<256>();
+        tc_fence_after();
+        if (half == 0 && row < rows) {
+            const float l = s_pair[0][row] + s_pair[1][row];
+            // a wait that ran out leaves NaN, which the answer then shows
+            my_stats[row] = s_failed ? make_float2(NAN, NAN)
+                            : l > 0.f || isnan(l) ? make_float2(ref, l)
+                                                  : make_float2(-INFINITY, 0.f);
+        }
+        if (!s_failed && busy) {
+            float* to = part + ((bh * p.splits + split) * a.R + row0 + row) * a.D;
+            for (int c = half * 16; c < a.D; c += 32) {
+                float o[16];
+                tmem_ld<16>(lanes + 2 * kTile + c, o);
+                if (row < rows)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4)
+                        *reinterpret_cast<float4*>(to + c + i) =
+                            make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
     }
 }
 
@@ -808,16 +1049,16 @@ bool attend_sizes_ok(int64_t B, int64_t Sq, int64_t Hq, int64_t Hkv, int64_t N, 
 AttendPlan make_plan(int64_t B, int64_t Sq, int64_t Hq, int64_t Hkv, int64_t N, int64_t D) {
     AttendPlan p{};
     const int64_t R = Sq * (Hq / Hkv), bh = B * Hkv;
-    p.rt = R <= 16 ? 16 : R <= 32 ? 32 : R <= 64 || D > 128 ? 64 : 128;
-    p.row_tiles = (int)((R + p.rt - 1) / p.rt);
     p.keep = R <= kKeepRows;
-    p.cols = D <= 128 ? 4 * p.rt : 8 * p.rt;  // logits of two tiles, and the outputs
+    p.rt = p.keep ? kKeepRows : 128;
+    p.row_tiles = (int)((R + p.rt - 1) / p.rt);
     const int subs = (int)(D + 63) / 64, stage = subs * kTile * 128;
-    // V^T is read 128 rows at a time: past an odd last block of 64 columns its (unused) rows
-    // are whatever follows, which has to be there
-    const int fixed = 1024 + subs * p.rt * 128 + p.rt * 512 + (subs % 2 ? kTile * 128 : 0);
-    // two blocks an SM where three stages fit half of it
-    const bool two = fixed + 3 * stage <= 112 * 1024;
+    // few rows: the weights too, and since V^T is read 128 rows at a time, past an odd last
+    // block of 64 columns its (unused) rows are whatever follows, which has to be there
+    const int fixed = 1024 + subs * p.rt * 128 +
+                      (p.keep ? p.rt * 512 + (subs % 2 ? kTile * 128 : 0) : 0);
+    // few rows: two blocks an SM where three stages fit half of it
+    const bool two = p.keep && fixed + 3 * stage <= 112 * 1024;
     const int room = (two ? 112 : kBlockSmem) * 1024 - fixed;
     p.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
     p.smem = fixed + p.stages * stage;
@@ -893,20 +1134,6 @@ bool cache_map(CUtensorMap* map, int dtype, const void* base, int64_t B, int64_t
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <class T, int RT, int CW>
-cudaError_t launch_split(const AttendArgs& a, const AttendPlan& p, const void* q,
-                         const CUtensorMap& k, const CUtensorMap& v, float2* stats, float* part,
-                         float* logits, cudaStream_t st) {
-    static std::atomic<unsigned long long> done{0};
-    once_per_device(done, [] {
-        cudaFuncSetAttribute(attend_split_kernel<T, RT, CW>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBlockSmem * 1024);
-    });
-    const int64_t blocks = (int64_t)a.B * a.Hkv * p.splits * p.row_tiles;
-    return launch_pdl(attend_split_kernel<T, RT, CW>, dim3((unsigned)blocks), dim3(64 + 128 * CW),
-                      (size_t)p.smem, st, a, p, (const T*)q, k, v, stats, part, logits);
-}
-
 template <class T>
 cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& p, const void* q,
                           const CUtensorMap& k, const CUtensorMap& v, char* ws,
@@ -918,10 +1145,20 @@ cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& p, const void* 
     cudaError_t e;
     {
         ProfScope prof("attend_split", st);
-        e = p.rt == 16   ? launch_split<T, 16, 1>(a, p, q, k, v, stats, part, logits, st)
-            : p.rt == 32 ? launch_split<T, 32, 2>(a, p, q, k, v, stats, part, logits, st)
-            : p.rt == 64 ? launch_split<T, 64, 2>(a, p, q, k, v, stats, part, logits, st)
-                         : launch_split<T, 128, 4>(a, p, q, k, v, stats, part, logits, st);
+        static std::atomic<unsigned long long> done{0};
+        once_per_device(done, [] {
+            cudaFuncSetAttribute(attend_narrow_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kBlockSmem * 1024);
+            cudaFuncSetAttribute(attend_wide_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kBlockSmem * 1024);
+            cudaFuncSetAttribute(attend_score_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kBlockSmem * 1024);
+        });
+        const dim3 blocks((unsigned)((int64_t)a.B * a.Hkv * p.splits * p.row_tiles));
+        e = p.keep ? launch_pdl(attend_narrow_kernel<T>, blocks, dim3(kNarrowThreads), (size_t)p.smem, st,
+                                a, p, (const T*)q, k, v, stats, part, logits)
+                   : launch_pdl(attend_wide_kernel<T>, blocks, dim3(kWideThreads), (size_t)p.smem, st, a,
+                                p, (const T*)q, k, v, stats, part);
     }
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)a.B * a.Hkv * a.R;
@@ -936,11 +1173,6 @@ cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& p, const void* 
     }
     if (e != cudaSuccess || p.keep) return e;
     ProfScope prof("attend_score", st);
-    static std::atomic<unsigned long long> done{0};
-    once_per_device(done, [] {
-        cudaFuncSetAttribute(attend_score_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kBlockSmem * 1024);
-    });
     const ScorePlan sp = make_score_plan((int64_t)a.B * a.Hkv, a.N, a.D);
     return launch_pdl(attend_score_kernel<T>, dim3((unsigned)((int64_t)a.B * a.Hkv * sp.blocks)),
                       dim3(kScoreThreads), (size_t)sp.smem, st, a, sp, (const T*)q, k,

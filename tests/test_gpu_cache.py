@@ -89,6 +89,37 @@ def test_attend_several_tokens(cuda_device, dtype, B, Sq, Hq, Hkv, N, D):
     check_attend(q, k, v, [max(0, N - 60 * (b + 1)) for b in range(B)], score)
 
 
+@pytest.mark.parametrize("Sq,Hq,Hkv,N,D", [(1, 8, 2, 30000, 128), (20, 4, 2, 24000, 64), (33, 8, 1, 9000, 128),
+                                           (5, 12, 1, 7000, 256), (3, 2, 2, 40000, 16)])
+def test_attend_long_runs(cuda_device, Sq, Hq, Hkv, N, D):
+    """Many key tiles to a block: every ring and buffer comes round several times.  Against
+    float64 on the device, at the tolerances of check_attend; a peak in the middle raises the
+    references late."""
+    B = 2
+    q, k, v, score = caches(N, B, Sq, Hq, Hkv, N, D, torch.bfloat16)
+    k[:, :, N // 2] = (q[:, 0, 0] * 3).to(k.dtype)[:, None]
+    q, k, v, score = (x.cuda() for x in (q, k, v, score))
+    n = torch.tensor([N, N - 333], dtype=torch.int32, device="cuda")
+    s = score.clone()
+    out = L.attend_accumulate(q, k, v, n, s)
+    G = Hq // Hkv
+    for b in range(B):
+        m = int(n[b])
+        see = torch.arange(m, device="cuda") <= (m - Sq + torch.arange(Sq, device="cuda"))[:, None]
+        for h in range(Hkv):
+            x = torch.einsum("igd,nd->gin", q[b].double()[:, h * G:(h + 1) * G], k[b, h, :m].double()) * D ** -0.5
+            p = torch.softmax(x.masked_fill(~see, -float("inf")), 2)
+            want = s.new_zeros(m, dtype=torch.float64) + score[b, h, :m].double() + p.sum((0, 1))
+            reach = float(q.abs().max() * k.abs().max()) * D ** 0.5
+            rel = (D * reach / 10 + 2 * reach + 64) * 2.0 ** -24
+            off = (s[b, h, :m].double() - want).abs() - rel * p.sum((0, 1)) - 2.0 ** -23 * want
+            assert off.max() <= Sq * G * 2.0 ** -126
+            o = torch.einsum("gin,nd->igd", p, v[b, h, :m].double())
+            tol = (rel + 2.0 ** -16) * float(v.abs().max()) + R.UNIT[q.dtype] * 1.01 * o.abs() + 2.0 ** -24
+            assert ((out[b, :, h * G:(h + 1) * G].double() - o).abs() <= tol).all()
+        assert torch.equal(s[b, :, m:], score[b, :, m:])
+
+
 def test_attend_empty_and_short_sequences(cuda_device):
     """Lengths of zero and one, shorter than Sq, beyond N and below 0."""
     q, k, v, score = caches(1, 6, 3, 4, 2, 150, 64, torch.bfloat16)
