@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     __shared__ bool s_seen[RT];
     __shared__ float s_slack;
     __shared__ alignas(16) int s_lim[RT];  // keys that each row sees, from the run's first
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = uniform((int)threadIdx.x >> 5);
     const int rt = blockIdx.x % p.row_tiles;
     const int64_t rest = blockIdx.x / p.row_tiles;
     const int split = (int)(rest % p.splits);
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     float2* my_stats = stats + (bh * p.splits + split) * a.R + row0;
 
     pdl_wait();
-    const int64_t n = cache_length(a, b);
+    const int64_t n = uniform(cache_length(a, b));
     // keys that the tile's last row sees, and this run's tiles among them
     int64_t seen = n - a.Sq + 1 + (row0 + rows - 1) / a.G;
     seen = seen < 0 ? 0 : seen;
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
     __syncthreads();
     tc_fence_after();
     // logits of two tiles, then the outputs of the weights' hi and lo parts
-    const uint32_t tmem = s_tmem, o_col = tmem + 2 * RT;
+    const uint32_t tmem = uniform(s_tmem), o_col = tmem + 2 * RT;
     // the ring's items: K0, K1, V0, K2, V1, ..., V(last)
     const int items = 2 * tiles;
     auto key_item = [](int t) { return t == 0 ? 0 : 2 * t - 1; };
@@ -293,28 +293,33 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                     mbar_wait(full + 8 * (i % p.stages), (i / p.stages) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        {
             const uint32_t shape_s = mma_shape(Pair<T>::bf16, false, false, kTile, RT);
             const uint32_t shape_o = mma_shape(Pair<T>::bf16, true, true, 128, 2 * RT);
             const uint64_t q_op = operand(q_at, 16, 1024, kSwizzle128);
             const uint64_t p_op = operand(p_at, 128, 2048, kNoSwizzle);
             auto logits_of = [&](int t) {  // S^T of tile t into its half
                 const int item = key_item(t), s = item % p.stages;
-                if (!mbar_wait(full + 8 * s, (item / p.stages) & 1)) return false;
+                if (!__all_sync(kAll, mbar_wait(full + 8 * s, (item / p.stages) & 1))) return false;
                 tc_fence_after();
-                key_products<RT>(tmem + (t & 1) * RT,
-                                 operand(ring + s * stage_bytes, 16, 1024, kSwizzle128), q_op, a.D,
-                                 shape_s);
-                mma_commit(empty + 8 * s);
-                mma_commit(s_done + 8 * (t & 1));
+                if (elect_one()) {
+                    key_products<RT>(tmem + (t & 1) * RT,
+                                     operand(ring + s * stage_bytes, 16, 1024, kSwizzle128), q_op,
+                                     a.D, shape_s);
+                    mma_commit(empty + 8 * s);
+                    mma_commit(s_done + 8 * (t & 1));
+                }
+                __syncwarp();
                 return true;
             };
             ok = logits_of(0) && (tiles == 1 || logits_of(1));
             for (int t = 0; t < tiles && ok; ++t) {
                 const int item = value_item(t), s = item % p.stages;
                 ok = mbar_wait(full + 8 * s, (item / p.stages) & 1) && mbar_wait(p_full, t & 1);
+                ok = __all_sync(kAll, ok);
                 if (!ok) break;
                 tc_fence_after();
+                if (elect_one()) {
                 for (int m = 0; m * 128 < a.D; ++m) {
                     const uint64_t v = operand(ring + s * stage_bytes + m * 2 * sub_bytes, sub_bytes,
                                                1024, kSwizzle128);
@@ -325,6 +330,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                 }
                 mma_commit(empty + 8 * s);
                 mma_commit(p_empty);
+                }
+                __syncwarp();
                 // the softmax has read tile t's half
                 if (t + 2 < tiles) ok = logits_of(t + 2);
             }
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     __shared__ uint32_t s_tmem;
     __shared__ int s_failed;
     __shared__ float s_pair[2][RT];  // what the two threads of a row tell each other
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = uniform((int)threadIdx.x >> 5);
     const int rt = blockIdx.x % p.row_tiles;
     const int64_t rest = blockIdx.x / p.row_tiles;
     const int split = (int)(rest % p.splits);
@@ -518,7 +525,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     float2* my_stats = stats + (bh * p.splits + split) * a.R + row0;
 
     pdl_wait();
-    const int64_t n = cache_length(a, b);
+    const int64_t n = uniform(cache_length(a, b));
     // keys that the tile's last row sees, and this run's tiles among them
     int64_t seen = n - a.Sq + 1 + (row0 + rows - 1) / a.G;
     seen = seen < 0 ? 0 : seen;
@@ -557,7 +564,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     __syncthreads();
     tc_fence_after();
     // logits (then weights) of two tiles, then the outputs
-    const uint32_t tmem = s_tmem, o_col = tmem + 2 * kTile;
+    const uint32_t tmem = uniform(s_tmem), o_col = tmem + 2 * kTile;
     // the ring's items: K0, K1, V0, K2, V1, ..., V(last)
     const int items = 2 * tiles;
     auto key_item = [](int t) { return t == 0 ? 0 : 2 * t - 1; };
@@ -585,26 +592,32 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     mbar_wait(full + 8 * (i % p.stages), (i / p.stages) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        {
             const uint32_t shape_s = mma_shape(Pair<T>::bf16, false, false, RT, kTile);
             const uint32_t shape_o = mma_shape(Pair<T>::bf16, false, true, RT, a.D);
             const uint64_t q_op = operand(q_at, 16, 1024, kSwizzle128);
             auto logits_of = [&](int t) {  // S of tile t into its half
                 const int item = key_item(t), s = item % p.stages;
-                if (!mbar_wait(full + 8 * s, (item / p.stages) & 1)) return false;
+                if (!__all_sync(kAll, mbar_wait(full + 8 * s, (item / p.stages) & 1))) return false;
                 tc_fence_after();
-                key_products<RT>(tmem + (t & 1) * kTile, q_op,
-                                 operand(ring + s * stage_bytes, 16, 1024, kSwizzle128), a.D, shape_s);
-                mma_commit(empty + 8 * s);
-                mma_commit(s_done + 8 * (t & 1));
+                if (elect_one()) {
+                    key_products<RT>(tmem + (t & 1) * kTile, q_op,
+                                     operand(ring + s * stage_bytes, 16, 1024, kSwizzle128), a.D,
+                                     shape_s);
+                    mma_commit(empty + 8 * s);
+                    mma_commit(s_done + 8 * (t & 1));
+                }
+                __syncwarp();
                 return true;
             };
             ok = logits_of(0) && (tiles == 1 || logits_of(1));
             for (int t = 0; t < tiles && ok; ++t) {
                 const int item = value_item(t), s = item % p.stages;
                 ok = mbar_wait(full + 8 * s, (item / p.stages) & 1) && mbar_wait(p_full + 8 * (t & 1), (t >> 1) & 1);
+                ok = __all_sync(kAll, ok);
                 if (!ok) break;
                 tc_fence_after();
+                if (elect_one()) {
                 // 16 keys at a time: 8 columns of weights; each half of the tile has its hi
                 // parts in 32 columns and its lo parts in the next 32
                 const uint64_t v = operand(ring + s * stage_bytes, sub_bytes, 1024, kSwizzle128);
@@ -616,8 +629,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 }
                 mma_commit(empty + 8 * s);
                 mma_commit(p_used);
+                }
+                __syncwarp();
                 // the next logits of this half go over weights that the product has read
-                if (t + 2 < tiles) ok = mbar_wait(p_used, t & 1) && logits_of(t + 2);
+                if (t + 2 < tiles) ok = __all_sync(kAll, mbar_wait(p_used, t & 1)) && logits_of(t + 2);
             }
         }
     } else {
@@ -900,11 +915,11 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
     __shared__ uint64_t bars[2 * kMaxStages + 5];
     __shared__ uint32_t s_tmem;
     __shared__ alignas(16) float s_log[kScoreRows];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = uniform((int)threadIdx.x >> 5);
     const int64_t bh = blockIdx.x / p.blocks;
     const int b = (int)(bh / a.Hkv), h = (int)(bh % a.Hkv);
     pdl_wait();
-    const int64_t n = cache_length(a, b);
+    const int64_t n = uniform(cache_length(a, b));
     // the sequence's tiles shared out evenly among its blocks
     const int64_t all = (n + kTile - 1) / kTile, per = (all + p.blocks - 1) / p.blocks;
     const int64_t first = blockIdx.x % p.blocks * per;
@@ -935,7 +950,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = uniform(s_tmem);
     bool ok = true;
     if (warp == 0) {
         if (lane == 0) {
@@ -955,25 +970,29 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
                     mbar_wait(full + 8 * (i % p.stages), (i / p.stages) & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        {
             const uint64_t q_op = operand(q_at, 16, 1024, kSwizzle128);
             int item = 0, turns[2] = {0, 0};
             for (int64_t rg = rg0; rg < rgs && ok; ++rg) {
                 const int rows = (int)(a.R - rg * kScoreRows < kScoreRows ? a.R - rg * kScoreRows : kScoreRows);
                 const uint32_t shape = mma_shape(Pair<T>::bf16, false, false, kTile, (rows + 31) & ~31);
-                ok = mbar_wait(q_full, (rg - rg0) & 1);
+                ok = __all_sync(kAll, mbar_wait(q_full, (rg - rg0) & 1));
                 for (int t = 0; t < tiles && ok; ++t, ++item) {
                     const int s = item % p.stages, half = t & 1;
                     ok = mbar_wait(full + 8 * s, (item / p.stages) & 1);
                     if (ok && turns[half] > 0) ok = mbar_wait(used + 8 * half, (turns[half] - 1) & 1);
+                    ok = __all_sync(kAll, ok);
                     if (!ok) break;
                     ++turns[half];
                     tc_fence_after();
+                    if (elect_one()) {
                     key_products<kScoreRows>(tmem + half * kScoreRows,
                                              operand(ring + s * tile_bytes, 16, 1024, kSwizzle128),
                                              q_op, a.D, shape);
                     mma_commit(empty + 8 * s);
                     mma_commit(done + 8 * half);
+                    }
+                    __syncwarp();
                 }
             }
         }
