@@ -14,7 +14,8 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
-from ._launch import DTYPES, distinct, extent, launch, need, overlap
+from ._launch import (DTYPES, distinct, extent, launch, need, no_gradient, overlap,
+                      strides_of)
 
 _HALF = (torch.bfloat16, torch.float16)
 _F32, _I32 = (torch.float32,), (torch.int32,)
@@ -29,13 +30,12 @@ def _check_caches(k, v, score, lengths, dtypes):
     need(lengths, "lengths", _I32, 1, dev)
     if v.shape != shape or score.shape != shape[:3] or lengths.shape[0] != shape[0]:
         raise ValueError("k and v must be (B, H, N, D), score (B, H, N) and lengths (B)")
-    strides = k.stride(), v.stride(), score.stride()
-    for s, n, name in zip(strides, (shape[3], shape[3], shape[2]), ("k", "v", "score")):
-        if s[-1] != 1 and n > 1:
+    for x, name in ((k, "k"), (v, "v"), (score, "score")):
+        if x.stride(-1) != 1 and x.shape[-1] > 1:
             raise ValueError(f"{name} must be consecutive in its last dimension")
     if not lengths.is_contiguous():
         raise ValueError("lengths must be contiguous")
-    return strides
+    return strides_of(k), strides_of(v), strides_of(score)
 
 
 def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths: torch.Tensor,
@@ -54,7 +54,8 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
     need(q, "q", (k.dtype,), 4, k.device)
     B, Sq, Hq, D = q.shape
     _, Hkv, N, _ = k.shape
-    qs = q.stride()
+    no_gradient("attend_accumulate", q, k, v, score)
+    qs = strides_of(q)
     if B != k.shape[0] or D != k.shape[3] or Hkv < 1 or Hq % Hkv != 0:
         raise ValueError("q must be (B, Sq, Hq, D) with Hq a multiple of the caches' heads")
     if D > 1 and qs[3] != 1:
@@ -63,7 +64,7 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
         score_out, outs = score, ss
     else:
         need(score_out, "score_out", _F32, 3, k.device)
-        outs = score_out.stride()
+        outs = strides_of(score_out)
         if score_out.shape != score.shape or N > 1 and outs[2] != 1:
             raise ValueError("score_out must have score's shape, consecutive in its last dimension")
         same = outs == ss and score_out.data_ptr() == score.data_ptr()
@@ -79,9 +80,9 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
             raise ValueError("out must be contiguous and have q's shape")
         if any(overlap(out, x) for x in (q, k, v, score, score_out)):
             raise ValueError("out must not overlap the inputs")
-    if B * Sq * Hq * D == 0:
-        if score_out is not score and B * Hkv * N > 0:
-            raise ValueError("nothing to attend with: Sq is 0")
+    if Sq < 1 or Hq < 1 or D < 1:
+        raise ValueError("q must hold at least one token, head and element")
+    if B == 0:
         return out
     if N == 0:
         return out.zero_()
@@ -118,6 +119,7 @@ def evict(k: torch.Tensor, v: torch.Tensor, score: torch.Tensor, lengths: torch.
     ``budget`` rows; rows from ``budget`` on are left as they were.  Rows that no key
     fills (fewer than ``budget`` in the cache) are 0 and their positions -1."""
     ks, vs, ss = _check_caches(k, v, score, lengths, DTYPES)
+    no_gradient("evict", k, v, score)
     B, H, N, D = k.shape
     budget, first, last = int(budget), int(first), int(last)
     if budget < 1 or first < 0 or last < 0 or first + last > budget:
@@ -147,8 +149,8 @@ def evict(k: torch.Tensor, v: torch.Tensor, score: torch.Tensor, lengths: torch.
             raise ValueError("the caches must hold at least one row of one element")
         left.copy_(lengths.clamp(0, min(N, budget)))
         return result
-    strides = _Strides16(*ks[:3], *vs[:3], *ss[:2], *ko.stride()[:3], *vo.stride()[:3],
-                         *so.stride()[:2])
+    strides = _Strides16(*ks[:3], *vs[:3], *ss[:2], *strides_of(ko)[:3],
+                         *strides_of(vo)[:3], *strides_of(so)[:2])
     launch(_lib().lapsum_evict, k.device, k.data_ptr(), v.data_ptr(), DTYPES[k.dtype],
            score.data_ptr(), lengths.data_ptr(), strides, B, H, N, D, budget, first, last,
            ko.data_ptr(), vo.data_ptr(), so.data_ptr(), positions.data_ptr(), left.data_ptr())

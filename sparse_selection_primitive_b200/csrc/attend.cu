@@ -32,7 +32,7 @@ constexpr int kKeepRows = 16;       // logits of more rows a key are formed agai
 constexpr int kMaxStages = 6;
 constexpr int kRunTiles = 16;
 constexpr int kBlockSmem = 223;     // KB of dynamic shared memory of a block that has an SM to itself
-constexpr int kJoinThreads = 256, kJoinKeys = 512;
+constexpr int kJoinThreads = 256, kJoinKeys = 1024;
 
 struct AttendArgs {
     int64_t qb, qh, qr;  // element strides of q: batch, head, token

@@ -168,6 +168,46 @@ def test_attend_score_out_and_scale(cuda_device):
     assert b is out and torch.equal(a, b) and torch.equal(s[0], into[0])
 
 
+def test_attend_single_dimensions_with_odd_strides(cuda_device):
+    """The stride of a dimension of one element means nothing."""
+    n = torch.tensor([90], dtype=torch.int32, device="cuda")
+    q, k, v, score = (x.cuda() for x in caches(8, 1, 1, 2, 1, 90, 64, torch.bfloat16))
+    odd = lambda x, s: x.as_strided(x.shape, s)  # noqa: E731
+    a = L.attend_accumulate(q, k, v, n, s1 := score.clone())
+    b = L.attend_accumulate(odd(q, (3, 7, 64, 1)), odd(k, (5, 9, 64, 1)), odd(v, (1, 1, 64, 1)), n,
+                            odd(s2 := score.clone(), (3, 3, 1)))
+    assert torch.equal(a, b) and torch.equal(s1, s2)
+    e = L.evict(k, v, score, n, 20)
+    f = L.evict(odd(k, (5, 9, 64, 1)), odd(v, (1, 1, 64, 1)), odd(score, (3, 3, 1)), n, 20)
+    assert all(torch.equal(x, y) for x, y in zip(e, f))
+
+
+def test_cache_calls_do_not_cut_graphs(cuda_device):
+    q, k, v, score = (x.cuda() for x in caches(9, 1, 1, 2, 1, 40, 64, torch.bfloat16))
+    n = torch.tensor([40], dtype=torch.int32, device="cuda")
+    q.requires_grad_(True)
+    with pytest.raises(RuntimeError):
+        L.attend_accumulate(q, k, v, n, score)
+    with torch.no_grad():
+        L.attend_accumulate(q, k, v, n, score)
+    k.requires_grad_(True)
+    with pytest.raises(RuntimeError):
+        L.evict(k, v, score, n, 4)
+    L.evict(k.detach(), v, score, n, 4)
+
+
+def test_cache_calls_on_empty_batches(cuda_device):
+    q, k, v, score = (x.cuda() for x in caches(10, 2, 1, 2, 1, 40, 64, torch.bfloat16))
+    n = torch.tensor([40, 40], dtype=torch.int32, device="cuda")
+    assert L.attend_accumulate(q[:0], k[:0], v[:0], n[:0], score[:0]).shape == (0, 1, 2, 64)
+    out = L.attend_accumulate(q, k[:, :, :0], v[:, :, :0], n, score[:, :, :0])
+    assert (out == 0).all()
+    with pytest.raises(ValueError):
+        L.attend_accumulate(q[:, :0], k, v, n, score)
+    e = L.evict(k[:0], v[:0], score[:0], n[:0], 4)
+    assert e.k.shape == (0, 1, 4, 64) and e.lengths.shape == (0,)
+
+
 def test_attend_sharp_and_flat_rows(cuda_device):
     """Logits hundreds apart (weights that underflow), equal keys, and one hot key in the last place."""
     q, k, v, score = caches(4, 1, 1, 4, 1, 600, 64, torch.bfloat16)

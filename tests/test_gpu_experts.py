@@ -286,6 +286,47 @@ def test_rows_strides_and_broadcast_gradients(cuda_device):
     assert torch.equal(only, two[1])
 
 
+def test_second_derivatives_are_refused(cuda_device):
+    """A backward pass that is itself recorded gives its gradient, but no second one."""
+    x = rows(40, 4, 16, torch.float32).requires_grad_(True)
+    w, _ = L.route_experts(x, 3)
+    g, = torch.autograd.grad(w.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
+
+
+def test_graph_of_a_backward_pass(cuda_device):
+    """Forward and backward captured together and replayed with other inputs."""
+    T, E, k, H = 20, 16, 3, 40
+    x, h = torch.zeros((T, E), device="cuda"), torch.zeros((T, H), device="cuda")
+    x.requires_grad_(True), h.requires_grad_(True)
+    dout = torch.randn((T, H), device="cuda")
+
+    def step(x, h):
+        w, i = L.route_experts(x, k, score="sigmoid")
+        p = L.expert_plan(i, E)
+        out = L.expert_combine(L.expert_gather(h, p) * 2, w, p)
+        return (out,) + torch.autograd.grad(out, (x, h), dout)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(x, h)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(x, h)
+    for seed in (3, 4):
+        gen = torch.Generator().manual_seed(seed)
+        a, b = torch.randn((T, E), generator=gen).cuda(), torch.randn((T, H), generator=gen).cuda()
+        with torch.no_grad():
+            x.copy_(a)
+            h.copy_(b)
+        graph.replay()
+        want = step(a.requires_grad_(True), b.requires_grad_(True))
+        assert all(torch.equal(u, v) for u, v in zip(got, want))
+
+
 def test_rows_refusals(cuda_device):
     p = L.expert_plan(assignments(1, 4, 2, 3).cuda(), 3)
     x = torch.zeros((4, 8), device="cuda")
