@@ -30,7 +30,7 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kTile = 128;          // keys per tile: the M of S^T
 constexpr int kKeepRows = 16;       // logits of more rows a key are formed again, not kept
 constexpr int kMaxStages = 6;
-constexpr int kRunTiles = 16;
+constexpr int kMostRuns = 296;      // runs of a head: two blocks for each of 148 SMs
 constexpr int kBlockSmem = 223;     // KB of dynamic shared memory of a block that has an SM to itself
 constexpr int kJoinThreads = 256, kJoinKeys = 1024;
 
@@ -1081,12 +1081,25 @@ AttendPlan make_plan(int64_t B, int64_t Sq, int64_t Hq, int64_t Hkv, int64_t N, 
     const int room = (two ? 112 : kBlockSmem) * 1024 - fixed;
     p.stages = room / stage < kMaxStages ? room / stage : kMaxStages;
     p.smem = fixed + p.stages * stage;
-    // Runs: one wave of blocks where the heads are few (less than half the slots); else
-    // runs of at most kRunTiles tiles, so that the last blocks to start are short
-    const int64_t tiles = (N + kTile - 1) / kTile, slots = 148 * (two ? 2 : 1);
-    int64_t splits = slots / (bh * p.row_tiles);
-    if (splits < 2) splits = (tiles + kRunTiles - 1) / kRunTiles;
-    p.splits = (int)(splits < tiles ? splits : tiles);
+    // Runs.  x blocks a run over `slots` places: with equal lengths they take whole waves of
+    // L tiles and a block's own time, with lengths between a fifth and all of N about 0.6 of
+    // that and one run more at the end; joining takes about 0.03 tiles a run.  The cheapest sum
+    // (the first counted twice) is taken.
+    const int64_t tiles = (N + kTile - 1) / kTile, slots = 148 * (two ? 2 : 1), x = bh * p.row_tiles;
+    const double own = p.keep ? 1.5 : 4.0;  // a block's start and end, in tiles
+    int64_t splits = 1;
+    double least = 1e300;
+    for (int64_t t = 1; t <= tiles && t <= kMostRuns; ++t) {
+        const double run = (double)((tiles + t - 1) / t), waves = (double)((x * t + slots - 1) / slots),
+                     even = waves * (run + own),
+                     uneven = (double)(x * t) / (double)slots * (0.6 * run + own) + run;
+        const double cost = 2.0 * even + uneven + 0.09 * (double)t;
+        if (cost < least) {
+            least = cost;
+            splits = t;
+        }
+    }
+    p.splits = (int)splits;
     p.RP = (R + 3) / 4 * 4;
     p.off_lse = up256((size_t)(bh * p.splits * R) * 8);
     p.off_part = p.off_lse + up256((size_t)(bh * R) * 4);
