@@ -8,6 +8,11 @@
 // read once and written to its k places, and a row of the result is summed from
 // its k places in the order j = 0 .. k - 1, so nothing depends on the order in
 // which blocks run.
+//
+// The rows are bound by DRAM: 16384 x 8 rows of 4 KB, gather 96 us (94 us of bytes at the copy
+// rate), combine 101 (94), backward of the combination 192 (177).  The plan of 131072
+// assignments takes 19 us in two launches, that of 512 takes 6 in one: chains of dependent
+// steps, with next to nothing to read.
 #include <atomic>
 #include <cstdint>
 #include <type_traits>

@@ -15,6 +15,11 @@
 // row in which two neighbouring ranks lie nearer than that bound is done again
 // with fp64 keys, so that the choice is always that of the fp64 keys; that is
 // rare unless the keys really are equal.
+//
+// What bounds it: instructions, not bytes.  16384 x 256 (8 chosen): 12.1 us for fp32 logits
+// (2.8 us of bytes), with 78% of the issue slots taken; 27.6 us for grouped sigmoid keys with
+// a bias (1.4 us of bytes).  Taking the largest out one by one, without the bound and the
+// ranking of take_largest, made these 18.6 and 60 us.
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -494,7 +499,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 //                 (softmax), times 1 - s_i (sigmoid), 0 elsewhere;
 //   softmax:      d_i = s_i (scale u_i [i chosen] - sum_j u_j w_j) on all experts;
 //   sigmoid:      d_i = u_i w_i (1 - s_i) on the chosen experts.
-// A row whose weights are NaN gets NaN.
+// A row whose weights are NaN gets NaN.  9.5 us for 16384 x 256 fp32 (2.8 us of bytes); carrying
+// the chosen terms to the lanes that own their experts instead of storing them on top took 19.
 template <class T, int V>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     route_backward_kernel(const T* logits, RouteArgs a, const float* weights,
