@@ -522,13 +522,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
         if (e >= 0) u = dw[t * a.k + lane];
     }
     bad = __any_sync(kAll, bad);
-    const float dot = warp_sum(e >= 0 ? u * w : 0.f);
+    // renormalised: with the shares w / scale, so that one expert's, 1, leaves exactly 0
+    const float dot = warp_sum(e >= 0 ? u * (a.renorm ? w / a.scale : w) : 0.f);
     float own = 0.f;  // this lane's chosen expert: its gradient, or (plain softmax) scale u
     const bool dense = !a.sigmoid && !a.renorm;
     if (e >= 0) {
         if (dense) own = a.scale * u;
         else {
-            own = w * (a.renorm ? u - dot / a.scale : u);
+            own = w * (a.renorm ? u - dot : u);
             if (a.sigmoid) own *= sigmoid_f(-widen(row[e]));  // 1 - s
         }
     }

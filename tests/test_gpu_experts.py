@@ -141,6 +141,15 @@ def test_route_strided_rows(cuda_device):
         check_route(big[::2, :64], 5)
 
 
+def test_route_gradient_of_a_single_expert_is_zero(cuda_device):
+    """One renormalised weight is the scale whatever the logits: its gradient is exactly 0."""
+    for how in (dict(scale=2.5), dict(score="sigmoid", scale=0.3)):
+        x = rows(18, 50, 24, torch.float32).requires_grad_(True)
+        w, _ = L.route_experts(x, 1, **how)
+        g, = torch.autograd.grad(w, x, torch.randn((50, 1), device="cuda"))
+        assert (w == torch.tensor(how["scale"], device="cuda")).all() and (g == 0).all()
+
+
 def test_route_refusals(cuda_device):
     x = rows(16, 4, 64, torch.float32)
     for bad in (dict(k=0), dict(k=33), dict(k=4, groups=5, top_groups=2),
