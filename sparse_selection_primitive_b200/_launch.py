@@ -42,6 +42,8 @@ def need(x, name: str, dtypes, dim: int, device=None):
 def extent(x: torch.Tensor):
     """First and one past the last byte that x's elements span."""
     start, span = x.data_ptr(), 1
+    if x.is_contiguous():
+        return start, start + x.numel() * x.element_size()
     for n, s in zip(x.shape, x.stride()):
         if n == 0:
             return start, start

@@ -330,6 +330,37 @@ def test_evict_long_rows(cuda_device, n, budget, kind):
         assert torch.equal(e.k[0, h], k[0, h, at]) and torch.equal(e.score[0, h], s[0, h, at])
 
 
+def test_caches_beyond_32_bit_offsets(cuda_device):
+    """A cache of more than 2^31 elements a head: one key near its end takes nearly all of the
+    weight, and the keys that stay lie near both ends."""
+    N, D = (1 << 24) + 4321, 128 + 16
+    assert N * D > 2 ** 31
+    k = torch.zeros((1, 1, N, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    v[0, 0, -4000:].normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    n = torch.tensor([N - 7], dtype=torch.int32, device="cuda")
+    hot = N - 1234
+    for Hq in (2, 20):      # both kernels: few and many rows a key
+        q = torch.full((1, 1, Hq, D), 1.0, dtype=torch.bfloat16, device="cuda")
+        k[0, 0, hot] = 5.0  # a logit of 5 sqrt(D) = 60 against 0: the others' weights sum to 2^24 e^-60
+        score = torch.zeros((1, 1, N), device="cuda")
+        out = L.attend_accumulate(q, k, v, n, score)
+        assert (out[0, 0] == v[0, 0, hot]).all()
+        # one weight of 1 (the others below 1e-18), off by the 20 roundings of its sum and Hq sums,
+        # and by those of its exponent: the logit is 60 log2(e) = 87 in powers of two, which the
+        # scaling, the row's log of the sum and their difference each round to 87 2^-24, times ln 2
+        assert abs(float(score[0, 0, hot]) - Hq) <= Hq * (Hq + 20 + 3 * 87 * 0.7) * 2.0 ** -24
+        assert float(score[0, 0, N - 7:].abs().max()) == 0
+        assert float(score[0, 0, :hot].max()) <= 1e-18
+    score = torch.zeros((1, 1, N), device="cuda")
+    want = [0, 1, 77, 1 << 22, N - 4000, hot, N - 9, N - 8]
+    score[0, 0, want[2:6]] = torch.tensor([1.0, 2.0, 3.0, 1.0], device="cuda")
+    e = L.evict(k, v, score, n, 8, first=2, last=2)
+    assert e.positions[0, 0].tolist() == want
+    at = torch.tensor(want, device="cuda")
+    assert torch.equal(e.k[0, 0], k[0, 0, at]) and torch.equal(e.v[0, 0], v[0, 0, at])
+
+
 def test_evict_short_rows(cuda_device):
     """Lengths of zero, one, the budget and one more; lengths beyond N and below 0."""
     k, v, s = evict_inputs(1, 7, 2, 64, 32, torch.float16)
