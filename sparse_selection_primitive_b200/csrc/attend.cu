@@ -139,10 +139,9 @@ __device__ __forceinline__ void load_rows(const AttendArgs& a, const T* q, int b
     }
 }
 
-// S^T = K Q^T of one tile: D / 16 steps along the rows of both operands, whose 128-byte
-// column blocks lie a tile of keys, or RT rows, apart.  One thread issues them, so it
-// only adds to the operands' descriptors: building one for each step took four times as
-// long as the step itself.
+// S^T = K Q^T of one tile (or S = Q K^T, with the operands exchanged): D / 16 steps along
+// the rows of both operands, whose 128-byte column blocks lie a tile of keys, or RT rows,
+// apart.  The steps only add to the operands' descriptors.
 template <int RT>
 __device__ __forceinline__ void key_products(uint32_t to, uint64_t k, uint64_t q, int D,
                                              uint32_t shape) {
@@ -299,33 +298,32 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                     mbar_wait(full + 8 * (i % p.stages), (i / p.stages) & 1);
         }
     } else if (warp == 1) {
-        {
-            const uint32_t shape_s = mma_shape(Pair<T>::bf16, false, false, kTile, RT);
-            const uint32_t shape_o = mma_shape(Pair<T>::bf16, true, true, 128, 2 * RT);
-            const uint64_t q_op = operand(q_at, 16, 1024, kSwizzle128);
-            const uint64_t p_op = operand(p_at, 128, 2048, kNoSwizzle);
-            auto logits_of = [&](int t) {  // S^T of tile t into its half
-                const int item = key_item(t), s = item % p.stages;
-                if (!__all_sync(kAll, mbar_wait(full + 8 * s, (item / p.stages) & 1))) return false;
-                tc_fence_after();
-                if (elect_one()) {
-                    key_products<RT>(tmem + (t & 1) * RT,
-                                     operand(ring + s * stage_bytes, 16, 1024, kSwizzle128), q_op,
-                                     a.D, shape_s);
-                    mma_commit(empty + 8 * s);
-                    mma_commit(s_done + 8 * (t & 1));
-                }
-                __syncwarp();
-                return true;
-            };
-            ok = logits_of(0) && (tiles == 1 || logits_of(1));
-            for (int t = 0; t < tiles && ok; ++t) {
-                const int item = value_item(t), s = item % p.stages;
-                ok = mbar_wait(full + 8 * s, (item / p.stages) & 1) && mbar_wait(p_full, t & 1);
-                ok = __all_sync(kAll, ok);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
+        const uint32_t shape_s = mma_shape(Pair<T>::bf16, false, false, kTile, RT);
+        const uint32_t shape_o = mma_shape(Pair<T>::bf16, true, true, 128, 2 * RT);
+        const uint64_t q_op = operand(q_at, 16, 1024, kSwizzle128);
+        const uint64_t p_op = operand(p_at, 128, 2048, kNoSwizzle);
+        auto logits_of = [&](int t) {  // S^T of tile t into its half
+            const int item = key_item(t), s = item % p.stages;
+            if (!__all_sync(kAll, mbar_wait(full + 8 * s, (item / p.stages) & 1))) return false;
+            tc_fence_after();
+            if (elect_one()) {
+                key_products<RT>(tmem + (t & 1) * RT,
+                                 operand(ring + s * stage_bytes, 16, 1024, kSwizzle128), q_op,
+                                 a.D, shape_s);
+                mma_commit(empty + 8 * s);
+                mma_commit(s_done + 8 * (t & 1));
+            }
+            __syncwarp();
+            return true;
+        };
+        ok = logits_of(0) && (tiles == 1 || logits_of(1));
+        for (int t = 0; t < tiles && ok; ++t) {
+            const int item = value_item(t), s = item % p.stages;
+            ok = mbar_wait(full + 8 * s, (item / p.stages) & 1) && mbar_wait(p_full, t & 1);
+            ok = __all_sync(kAll, ok);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
                 for (int m = 0; m * 128 < a.D; ++m) {
                     const uint64_t v = operand(ring + s * stage_bytes + m * 2 * sub_bytes, sub_bytes,
                                                1024, kSwizzle128);
@@ -336,11 +334,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                 }
                 mma_commit(empty + 8 * s);
                 mma_commit(p_empty);
-                }
-                __syncwarp();
-                // the softmax has read tile t's half
-                if (t + 2 < tiles) ok = logits_of(t + 2);
             }
+            __syncwarp();
+            // the softmax has read tile t's half
+            if (t + 2 < tiles) ok = logits_of(t + 2);
         }
     } else {
         const int quarter = warp & 3;                  // the lanes of tensor memory it may read
@@ -598,32 +595,32 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     mbar_wait(full + 8 * (i % p.stages), (i / p.stages) & 1);
         }
     } else if (warp == 1) {
-        {
-            const uint32_t shape_s = mma_shape(Pair<T>::bf16, false, false, RT, kTile);
-            const uint32_t shape_o = mma_shape(Pair<T>::bf16, false, true, RT, a.D);
-            const uint64_t q_op = operand(q_at, 16, 1024, kSwizzle128);
-            auto logits_of = [&](int t) {  // S of tile t into its half
-                const int item = key_item(t), s = item % p.stages;
-                if (!__all_sync(kAll, mbar_wait(full + 8 * s, (item / p.stages) & 1))) return false;
-                tc_fence_after();
-                if (elect_one()) {
-                    key_products<RT>(tmem + (t & 1) * kTile, q_op,
-                                     operand(ring + s * stage_bytes, 16, 1024, kSwizzle128), a.D,
-                                     shape_s);
-                    mma_commit(empty + 8 * s);
-                    mma_commit(s_done + 8 * (t & 1));
-                }
-                __syncwarp();
-                return true;
-            };
-            ok = logits_of(0) && (tiles == 1 || logits_of(1));
-            for (int t = 0; t < tiles && ok; ++t) {
-                const int item = value_item(t), s = item % p.stages;
-                ok = mbar_wait(full + 8 * s, (item / p.stages) & 1) && mbar_wait(p_full + 8 * (t & 1), (t >> 1) & 1);
-                ok = __all_sync(kAll, ok);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
+        const uint32_t shape_s = mma_shape(Pair<T>::bf16, false, false, RT, kTile);
+        const uint32_t shape_o = mma_shape(Pair<T>::bf16, false, true, RT, a.D);
+        const uint64_t q_op = operand(q_at, 16, 1024, kSwizzle128);
+        auto logits_of = [&](int t) {  // S of tile t into its half
+            const int item = key_item(t), s = item % p.stages;
+            if (!__all_sync(kAll, mbar_wait(full + 8 * s, (item / p.stages) & 1))) return false;
+            tc_fence_after();
+            if (elect_one()) {
+                key_products<RT>(tmem + (t & 1) * kTile, q_op,
+                                 operand(ring + s * stage_bytes, 16, 1024, kSwizzle128), a.D,
+                                 shape_s);
+                mma_commit(empty + 8 * s);
+                mma_commit(s_done + 8 * (t & 1));
+            }
+            __syncwarp();
+            return true;
+        };
+        ok = logits_of(0) && (tiles == 1 || logits_of(1));
+        for (int t = 0; t < tiles && ok; ++t) {
+            const int item = value_item(t), s = item % p.stages;
+            ok = mbar_wait(full + 8 * s, (item / p.stages) & 1) &&
+                 mbar_wait(p_full + 8 * (t & 1), (t >> 1) & 1);
+            ok = __all_sync(kAll, ok);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
                 // 16 keys at a time: 8 columns of weights; each half of the tile has its hi
                 // parts in 32 columns and its lo parts in the next 32
                 const uint64_t v = operand(ring + s * stage_bytes, sub_bytes, 1024, kSwizzle128);
@@ -635,11 +632,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 }
                 mma_commit(empty + 8 * s);
                 mma_commit(p_used);
-                }
-                __syncwarp();
-                // the next logits of this half go over weights that the product has read
-                if (t + 2 < tiles) ok = __all_sync(kAll, mbar_wait(p_used, t & 1)) && logits_of(t + 2);
             }
+            __syncwarp();
+            // the next logits of this half go over weights that the product has read
+            if (t + 2 < tiles) ok = __all_sync(kAll, mbar_wait(p_used, t & 1)) && logits_of(t + 2);
         }
     } else {
         const int quarter = warp & 3, half = (warp - 2) / 4;
@@ -976,30 +972,28 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
                     mbar_wait(full + 8 * (i % p.stages), (i / p.stages) & 1);
         }
     } else if (warp == 1) {
-        {
-            const uint64_t q_op = operand(q_at, 16, 1024, kSwizzle128);
-            int item = 0, turns[2] = {0, 0};
-            for (int64_t rg = rg0; rg < rgs && ok; ++rg) {
-                const int rows = (int)(a.R - rg * kScoreRows < kScoreRows ? a.R - rg * kScoreRows : kScoreRows);
-                const uint32_t shape = mma_shape(Pair<T>::bf16, false, false, kTile, (rows + 31) & ~31);
-                ok = __all_sync(kAll, mbar_wait(q_full, (rg - rg0) & 1));
-                for (int t = 0; t < tiles && ok; ++t, ++item) {
-                    const int s = item % p.stages, half = t & 1;
-                    ok = mbar_wait(full + 8 * s, (item / p.stages) & 1);
-                    if (ok && turns[half] > 0) ok = mbar_wait(used + 8 * half, (turns[half] - 1) & 1);
-                    ok = __all_sync(kAll, ok);
-                    if (!ok) break;
-                    ++turns[half];
-                    tc_fence_after();
-                    if (elect_one()) {
+        const uint64_t q_op = operand(q_at, 16, 1024, kSwizzle128);
+        int item = 0, turns[2] = {0, 0};
+        for (int64_t rg = rg0; rg < rgs && ok; ++rg) {
+            const int rows = (int)(a.R - rg * kScoreRows < kScoreRows ? a.R - rg * kScoreRows : kScoreRows);
+            const uint32_t shape = mma_shape(Pair<T>::bf16, false, false, kTile, (rows + 31) & ~31);
+            ok = __all_sync(kAll, mbar_wait(q_full, (rg - rg0) & 1));
+            for (int t = 0; t < tiles && ok; ++t, ++item) {
+                const int s = item % p.stages, half = t & 1;
+                ok = mbar_wait(full + 8 * s, (item / p.stages) & 1);
+                if (ok && turns[half] > 0) ok = mbar_wait(used + 8 * half, (turns[half] - 1) & 1);
+                ok = __all_sync(kAll, ok);
+                if (!ok) break;
+                ++turns[half];
+                tc_fence_after();
+                if (elect_one()) {
                     key_products<kScoreRows>(tmem + half * kScoreRows,
                                              operand(ring + s * tile_bytes, 16, 1024, kSwizzle128),
                                              q_op, a.D, shape);
                     mma_commit(empty + 8 * s);
                     mma_commit(done + 8 * half);
-                    }
-                    __syncwarp();
                 }
+                __syncwarp();
             }
         }
     } else {
