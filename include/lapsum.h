@@ -527,7 +527,7 @@ int lapsum_expert_combine_backward(const void* dout, int dtype, int64_t ld, cons
  * hold anything.  `strides` (host, 13 entries, in elements): batch, head and token
  * stride of q; batch, head and row stride of k, then of v; batch and head stride
  * of score_in, then of score_out (the elements of a row, and a head's scores, are
- * consecutive).  D is a multiple of 16 up to 256; q, k, v and out are 16-byte
+ * consecutive; the stride of a dimension of one element is not read).  D is a multiple of 16 up to 256; q, k, v and out are 16-byte
  * aligned and their strides multiples of 8; Hq a multiple of Hkv.  Softmax
  * statistics, sums and scores are fp32.  ws: lapsum_attend_workspace_bytes(...)
  * bytes, 256-byte aligned (0: bad sizes).
@@ -551,7 +551,8 @@ int lapsum_attend_accumulate(const void* q, const void* k, const void* v, int dt
  * cache rows from `budget` on are left as they were.  Rows are D elements of
  * `dtype`.  `strides` (host, 16 entries, in elements): batch, head and row stride
  * of k, then of v; batch and head stride of score; the same eight of k_out,
- * v_out and score_out.  The outputs must not overlap the inputs.  first + last <= budget.
+ * v_out and score_out (not read for dimensions of one element).  The outputs must not
+ * overlap the inputs.  first + last <= budget.
  */
 int lapsum_evict(const void* k, const void* v, int dtype, const float* score,
                  const int32_t* lengths, const int64_t* strides, int64_t B, int64_t H, int64_t N,

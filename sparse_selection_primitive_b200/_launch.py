@@ -68,14 +68,9 @@ def distinct(x: torch.Tensor) -> bool:
     return True
 
 
-def strides_of(x: torch.Tensor):
-    """x's strides, 0 for dimensions of one element (whose stride means nothing)."""
-    s = x.stride()
-    return s if 1 not in x.shape else tuple(0 if n == 1 else t for n, t in zip(x.shape, s))
-
-
-def no_gradient(name: str, *tensors):
-    """A call without a backward pass must not cut a graph unnoticed."""
-    if torch.is_grad_enabled() and any(x.requires_grad for x in tensors):
+def no_gradient(name: str):
+    """Refuses tensors that require a gradient: a call without a backward pass must not cut
+    a graph unnoticed."""
+    if torch.is_grad_enabled():
         raise RuntimeError(f"{name} has no gradient: call it under torch.no_grad() or on "
                            "detached tensors")

@@ -9,13 +9,13 @@ name (gist.science explainer pages, section 4.2).
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 import torch
 
 from . import _lib
-from ._launch import (DTYPES, distinct, extent, launch, need, no_gradient, overlap,
-                      strides_of)
+from ._launch import DTYPES, distinct, extent, launch, need, no_gradient, overlap
 
 _HALF = (torch.bfloat16, torch.float16)
 _F32, _I32 = (torch.float32,), (torch.int32,)
@@ -30,12 +30,17 @@ def _check_caches(k, v, score, lengths, dtypes):
     need(lengths, "lengths", _I32, 1, dev)
     if v.shape != shape or score.shape != shape[:3] or lengths.shape[0] != shape[0]:
         raise ValueError("k and v must be (B, H, N, D), score (B, H, N) and lengths (B)")
-    for x, name in ((k, "k"), (v, "v"), (score, "score")):
-        if x.stride(-1) != 1 and x.shape[-1] > 1:
-            raise ValueError(f"{name} must be consecutive in its last dimension")
+    ks, vs, ss = k.stride(), v.stride(), score.stride()
+    if (ks[3] != 1 or vs[3] != 1) and shape[3] > 1 or ss[2] != 1 and shape[2] > 1:
+        raise ValueError("k, v and score must be consecutive in their last dimension")
     if not lengths.is_contiguous():
         raise ValueError("lengths must be contiguous")
-    return strides_of(k), strides_of(v), strides_of(score)
+    return ks, vs, ss
+
+
+@functools.lru_cache(maxsize=256)
+def _attend_workspace_bytes(B, Sq, Hq, Hkv, N, D) -> int:
+    return _lib().lapsum_attend_workspace_bytes(B, Sq, Hq, Hkv, N, D)
 
 
 def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths: torch.Tensor,
@@ -54,8 +59,9 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
     need(q, "q", (k.dtype,), 4, k.device)
     B, Sq, Hq, D = q.shape
     _, Hkv, N, _ = k.shape
-    no_gradient("attend_accumulate", q, k, v, score)
-    qs = strides_of(q)
+    if q.requires_grad or k.requires_grad or v.requires_grad or score.requires_grad:
+        no_gradient("attend_accumulate")
+    qs = q.stride()
     if B != k.shape[0] or D != k.shape[3] or Hkv < 1 or Hq % Hkv != 0:
         raise ValueError("q must be (B, Sq, Hq, D) with Hq a multiple of the caches' heads")
     if D > 1 and qs[3] != 1:
@@ -64,7 +70,7 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
         score_out, outs = score, ss
     else:
         need(score_out, "score_out", _F32, 3, k.device)
-        outs = strides_of(score_out)
+        outs = score_out.stride()
         if score_out.shape != score.shape or N > 1 and outs[2] != 1:
             raise ValueError("score_out must have score's shape, consecutive in its last dimension")
         same = outs == ss and score_out.data_ptr() == score.data_ptr()
@@ -73,7 +79,7 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
     if not distinct(score_out):
         raise ValueError("the scores written must not share memory")
     if out is None:
-        out = torch.empty((B, Sq, Hq, D), dtype=q.dtype, device=q.device)
+        out = q.new_empty(q.shape)
     else:
         need(out, "out", (q.dtype,), 4, q.device)
         if out.shape != q.shape or not out.is_contiguous():
@@ -88,10 +94,9 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
         return out.zero_()
     strides = _Strides13(qs[0], qs[2], qs[1], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2], ss[0],
                          ss[1], outs[0], outs[1])
-    lib = _lib()
-    nbytes = lib.lapsum_attend_workspace_bytes(B, Sq, Hq, Hkv, N, D)
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=q.device)
-    launch(lib.lapsum_attend_accumulate, q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    nbytes = _attend_workspace_bytes(B, Sq, Hq, Hkv, N, D)
+    ws = q.new_empty(nbytes // 2)  # two bytes an element
+    launch(_lib().lapsum_attend_accumulate, q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(),
            DTYPES[q.dtype], lengths.data_ptr(), strides, B, Sq, Hq, Hkv, N, D,
            D ** -0.5 if scale is None else float(scale), score.data_ptr(), score_out.data_ptr(),
            out.data_ptr(), ws.data_ptr(), nbytes)
@@ -119,15 +124,16 @@ def evict(k: torch.Tensor, v: torch.Tensor, score: torch.Tensor, lengths: torch.
     ``budget`` rows; rows from ``budget`` on are left as they were.  Rows that no key
     fills (fewer than ``budget`` in the cache) are 0 and their positions -1."""
     ks, vs, ss = _check_caches(k, v, score, lengths, DTYPES)
-    no_gradient("evict", k, v, score)
+    if k.requires_grad or v.requires_grad or score.requires_grad:
+        no_gradient("evict")
     B, H, N, D = k.shape
     budget, first, last = int(budget), int(first), int(last)
     if budget < 1 or first < 0 or last < 0 or first + last > budget:
         raise ValueError("budget must be at least 1, and first + last at most budget")
     if out is None:
-        ko = torch.empty((B, H, budget, D), dtype=k.dtype, device=k.device)
+        ko = k.new_empty((B, H, budget, D))
         vo = torch.empty_like(ko)
-        so = torch.empty((B, H, budget), dtype=torch.float32, device=k.device)
+        so = score.new_empty((B, H, budget))
     else:
         ko, vo, so = out
         need(ko, "out[0]", (k.dtype,), 4, k.device)
@@ -141,16 +147,16 @@ def evict(k: torch.Tensor, v: torch.Tensor, score: torch.Tensor, lengths: torch.
         if any(overlap(x, y) for x in (ko, vo, so) for y in (k, v, score, lengths)) or \
                 extent(ko) == extent(vo):
             raise ValueError("out must not overlap the inputs")
-    positions = torch.empty((B, H, budget), dtype=torch.int32, device=k.device)
-    left = torch.empty(B, dtype=torch.int32, device=k.device)
+    positions = lengths.new_empty((B, H, budget))
+    left = torch.empty_like(lengths)
     result = Evicted(ko, vo, so, positions, left)
     if B * H * D == 0 or N == 0:
         if B * H > 0:
             raise ValueError("the caches must hold at least one row of one element")
         left.copy_(lengths.clamp(0, min(N, budget)))
         return result
-    strides = _Strides16(*ks[:3], *vs[:3], *ss[:2], *strides_of(ko)[:3],
-                         *strides_of(vo)[:3], *strides_of(so)[:2])
+    strides = _Strides16(*ks[:3], *vs[:3], *ss[:2], *ko.stride()[:3], *vo.stride()[:3],
+                         *so.stride()[:2])
     launch(_lib().lapsum_evict, k.device, k.data_ptr(), v.data_ptr(), DTYPES[k.dtype],
            score.data_ptr(), lengths.data_ptr(), strides, B, H, N, D, budget, first, last,
            ko.data_ptr(), vo.data_ptr(), so.data_ptr(), positions.data_ptr(), left.data_ptr())

@@ -1232,8 +1232,14 @@ extern "C" int lapsum_attend_accumulate(const void* q, const void* k, const void
         return LAPSUM_EINVAL;
     if (dtype != LAPSUM_DTYPE_BF16 && dtype != LAPSUM_DTYPE_F16) return LAPSUM_EINVAL;
     if (!attend_sizes_ok(B, Sq, Hq, Hkv, N, D) || !std::isfinite(scale)) return LAPSUM_EINVAL;
-    for (int i = 0; i < 13; ++i)
-        if (strides[i] < 0 || (i < 9 && strides[i] % 8 != 0)) return LAPSUM_EINVAL;
+    // the stride of a dimension of one element means nothing
+    const int64_t size[13] = {B, Hq, Sq, B, Hkv, N, B, Hkv, N, B, Hkv, B, Hkv};
+    int64_t own[13];
+    for (int i = 0; i < 13; ++i) {
+        own[i] = size[i] > 1 ? strides[i] : 0;
+        if (own[i] < 0 || (i < 9 && own[i] % 8 != 0)) return LAPSUM_EINVAL;
+    }
+    strides = own;
     // rows of one cache may repeat over heads and sequences, but not over its keys
     if (N > 1 && (strides[5] < D || strides[8] < D)) return LAPSUM_EINVAL;
     if (!aligned_to(q, 16) || !aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(out, 16) ||

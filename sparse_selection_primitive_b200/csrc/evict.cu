@@ -528,8 +528,14 @@ extern "C" int lapsum_evict(const void* k, const void* v, int dtype, const float
     if (budget < 1 || budget >= big || first < 0 || last < 0 || first > budget ||
         last > budget - first)
         return LAPSUM_EINVAL;
-    for (int i = 0; i < 16; ++i)
-        if (strides[i] < 0) return LAPSUM_EINVAL;
+    // the stride of a dimension of one element means nothing
+    const int64_t extent[16] = {B, H, N, B, H, N, B, H, B, H, budget, B, H, budget, B, H};
+    int64_t own[16];
+    for (int i = 0; i < 16; ++i) {
+        own[i] = extent[i] > 1 ? strides[i] : 0;
+        if (own[i] < 0) return LAPSUM_EINVAL;
+    }
+    strides = own;
     const int size = dtype_size(dtype);
     if (!aligned_to(k, size) || !aligned_to(v, size) || !aligned_to(k_out, size) ||
         !aligned_to(v_out, size) || !aligned_to(score, 4) || !aligned_to(score_out, 4) ||
