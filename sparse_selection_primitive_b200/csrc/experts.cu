@@ -347,6 +347,11 @@ cudaError_t with_pack(size_t align, int64_t H, int64_t ld, F f) {
     return f(std::integral_constant<int, 1>{});
 }
 
+// Threads that a row of H elements keeps busy at 16 bytes each.
+template <class T, int W>
+int64_t row_threads(int64_t H) {
+    return (H / W + packs_of<T, W>() - 1) / packs_of<T, W>();
+}
 // Threads to a row: `threads`, up to a power of two, `least` at least.
 RowArgs row_args(int64_t ld, int64_t T, int32_t k, int64_t H, const int32_t* slots,
                  const int32_t* live, int64_t threads, int least) {
@@ -432,7 +437,7 @@ extern "C" int lapsum_expert_gather(const void* x, int dtype, int64_t ld, int64_
         using E = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
         return with_pack<E>(address_bits(x) | address_bits(xs), H, ld, [&](auto w) {
             constexpr int W = decltype(w)::value;
-            const RowArgs a = row_args(ld, T, k, H, slots, live, (H / W + packs_of<E, W>() - 1) / packs_of<E, W>(), 1);
+            const RowArgs a = row_args(ld, T, k, H, slots, live, row_threads<E, W>(H), 1);
             return launch_pdl(expert_gather_kernel<E, W>, row_grid(a, 1 << 20), dim3(kRowThreads), 0, st, a,
                               (const E*)x, (E*)xs);
         });
@@ -455,7 +460,7 @@ extern "C" int lapsum_expert_combine(const void* y, int dtype, int64_t T, int32_
         using E = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
         return with_pack<E>(address_bits(y) | address_bits(out), H, H, [&](auto w) {
             constexpr int W = decltype(w)::value;
-            const RowArgs a = row_args(H, T, k, H, slots, live, (H / W + packs_of<E, W>() - 1) / packs_of<E, W>(), 1);
+            const RowArgs a = row_args(H, T, k, H, slots, live, row_threads<E, W>(H), 1);
             return launch_pdl(expert_combine_kernel<E, W>, row_grid(a, 16), dim3(kRowThreads), 0, st, a,
                               (const E*)y, weights, (E*)out);
         });
