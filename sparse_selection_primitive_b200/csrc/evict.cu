@@ -9,9 +9,10 @@
 // of plain samples); one pass over the row then marks the keys above the range in a bit map
 // and lists those inside, and the boundary is found in the list by radix selection.
 // Counts prove the range right; where they do not, or where the list would
-// overflow, histogram passes over the row narrow the range first.  The kept positions
-// come out of the bit map in order, so nothing is sorted; keys equal to the boundary
-// have a bit map of their own, of which the first (lowest positions) are taken.
+// overflow, histogram passes over the row narrow the range first, three at most
+// (select_range.cuh).  The kept positions come out of the bit map in order, so nothing is
+// sorted; keys equal to the boundary have a bit map of their own, of which the first
+// (lowest positions) are taken.
 // Gathering: one thread per 16 bytes of a kept row, over all rows at once.
 //
 // 256 x 65536 (lengths from a quarter of that) to 1024: selection 35 us (7 us of bytes), of
@@ -27,15 +28,14 @@
 #include "elements.cuh"
 #include "lapsum_common.cuh"
 #include "lapsum_kernels.h"
+#include "select_range.cuh"
 
 namespace lapsum {
 namespace {
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelBits = 11, kSelBins = 1 << kSelBits;
 constexpr int kSelSample = 2 * kSelThreads;
-constexpr int kSelList = 8192;
 constexpr int64_t kSelWindow = int64_t(1) << 18;  // positions that the bit maps hold at a time
 static_assert(kSelSample <= kSelList, "the sample is sorted where the list will stand");
 constexpr unsigned kAll = 0xffffffffu;
@@ -48,11 +48,6 @@ struct EvictArgs {
     const float* score;
     const int32_t* lengths;
 };
-
-// NaN sorts below every number (its weight is unknown), -0 as +0.
-__device__ __forceinline__ uint32_t score_key(float s) {
-    return isnan(s) ? 0u : to_key(s + 0.f);
-}
 
 __device__ __forceinline__ int64_t row_length(const EvictArgs& a, int64_t b) {
     const int64_t n = a.lengths[b];
@@ -89,13 +84,6 @@ __device__ __forceinline__ int2 block_prefix(int2 v, int2* tot, int2* sums) {
     return make_int2(before.x + inc.x - v.x, before.y + inc.y - v.y);
 }
 
-// What the block knows about its row's boundary: it is the need-th largest key of the
-// competitors, `above` of them lie above hi and `inside` in [lo, hi].
-struct Range {
-    uint32_t lo, hi;
-    int above, inside;
-};
-
 struct SelShared {
     alignas(16) unsigned hist[kSelBins];
     int2 sums[kSelWarps];
@@ -103,12 +91,6 @@ struct SelShared {
     int listed;               // keys listed (may exceed the room)
     int above;
 };
-
-// Bin of a key of [lo, hi] when the range is cut into at most kSelBins bins.
-__device__ __forceinline__ int range_shift(uint32_t lo, uint32_t hi) {
-    const int bits = 32 - __clz(hi - lo);  // 0 for a single key
-    return bits > kSelBits ? bits - kSelBits : 0;
-}
 
 // Adds one to a bin; a warp whose active lanes all want the same bin adds once.
 __device__ __forceinline__ void count_bin(unsigned* hist, int bin) {
@@ -127,7 +109,6 @@ __device__ __forceinline__ void count_bin(unsigned* hist, int bin) {
 __device__ void narrow_range(SelShared& sh, int need) {
     __syncthreads();
     const Range g = sh.range;
-    const int shift = range_shift(g.lo, g.hi);
     // thread t owns four neighbouring bins, the highest ones first
     static_assert(kSelBins == 4 * kSelThreads, "four bins a thread");
     const int bin0 = kSelBins - 4 - 4 * (int)threadIdx.x;
@@ -137,11 +118,7 @@ __device__ void narrow_range(SelShared& sh, int need) {
     int at = g.above + block_prefix(make_int2(c[0] + c[1] + c[2] + c[3], 0), &tot, sh.sums).x;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (at < need && need <= at + c[i]) {
-            const uint32_t lo = g.lo + ((uint32_t)(bin0 + 3 - i) << shift);
-            const uint64_t hi = (uint64_t)lo + (1ull << shift) - 1;
-            sh.range = Range{lo, hi < g.hi ? (uint32_t)hi : g.hi, at, c[i]};
-        }
+        if (at < need && need <= at + c[i]) sh.range = range_of_bin(g, bin0 + 3 - i, at, c[i]);
         at += c[i];
     }
     __syncthreads();
@@ -221,16 +198,13 @@ __device__ void sample_range(SelShared& sh, uint32_t* sorted, const float* score
 // The marking pass over the competitors [lo, hi): bits of `above` for the keys above
 // g.hi (not when it is null), and the positions of the keys in [g.lo, g.hi] listed as far
 // as the list has room; sh.above and sh.listed count them.  A thread compares four runs
-// of four positions with the range, as floats (the order of the keys, NaN apart), while the
-// next four are on their way; its warp makes room for all its finds with one addition.
+// of four positions with the range, as floats (range_test), while the next four are on their
+// way; its warp makes room for all its finds with one addition.
 __device__ void mark_and_list(SelShared& sh, const float* score, int64_t lo, int64_t hi, Range g,
                               uint32_t* above, int32_t* list_at) {
     constexpr int kRuns = 4;
     const int lane = threadIdx.x & 31;
-    const bool all = g.lo == 0u;  // then NaN too
-    const float floor = from_key(g.lo);
-    // past +inf no number lies above the range
-    const float ceil = g.hi < 0xff800000u ? from_key(g.hi) : INFINITY;
+    const RangeTest is = range_test(g);
     unsigned over = 0;
     // at: position of v[0].x, the runs `step` positions apart; use: bit 4 u + j for each
     // value that counts
@@ -241,11 +215,11 @@ __device__ void mark_and_list(SelShared& sh, const float* score, int64_t lo, int
             const float x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (x[j] >= floor) in |= 1u << (4 * u + j);
-                if (x[j] > ceil) top |= 1u << (4 * u + j);
+                if (x[j] >= is.floor) in |= 1u << (4 * u + j);
+                if (x[j] >= is.over) top |= 1u << (4 * u + j);
             }
         }
-        if (all) in = 0xffffu;
+        if (is.all) in = 0xffffu;
         in &= use & ~top;
         top &= use;
         over += __popc(top);
@@ -311,6 +285,52 @@ __device__ void mark_and_list(SelShared& sh, const float* score, int64_t lo, int
     if (over) atomicAdd(&sh.above, (int)over);
 }
 
+// The steps of settle_range on one row; every thread calls them.
+struct BoundarySearch {
+    SelShared& sh;
+    const float* score;
+    int64_t lo, hi;
+    int need, competitors;
+    int64_t words;        // of a bit map of the row
+    uint32_t *above_map;  // null: the row is longer than the bit maps
+    uint32_t* tie_map;
+    int32_t* list_at;
+
+    __device__ __forceinline__ Range range() const { return sh.range; }
+    __device__ __forceinline__ void set(Range g) {
+        __syncthreads();
+        if (threadIdx.x == 0) sh.range = g;
+        __syncthreads();
+    }
+    __device__ __forceinline__ Range mark() {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            sh.listed = 0;
+            sh.above = 0;
+        }
+        if (above_map != nullptr) {
+            clear_words(above_map, words);
+            clear_words(tie_map, words);
+        }
+        __syncthreads();
+        const Range g = sh.range;
+        mark_and_list(sh, score, lo, hi, g, above_map, list_at);
+        __syncthreads();
+        return Range{g.lo, g.hi, sh.above, sh.listed};
+    }
+    __device__ __forceinline__ void narrow() {
+        __syncthreads();
+        clear_words(sh.hist, kSelBins);
+        __syncthreads();
+        const Range g = sh.range;
+        const int shift = range_shift(g.lo, g.hi);
+        each_key(score, lo, hi, [&](int64_t, uint32_t key) {
+            if (key >= g.lo && key <= g.hi) count_bin(sh.hist, (int)((key - g.lo) >> shift));
+        });
+        narrow_range(sh, need);
+    }
+};
+
 __global__ void __launch_bounds__(kSelThreads, 2)
     evict_select_kernel(EvictArgs a, int64_t window, int32_t* positions, int32_t* lengths_out) {
     pdl_wait();
@@ -335,7 +355,6 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     const int need = (int)(a.budget - a.first - a.last);
     const bool one = n <= window;                 // the whole row fits the bit maps
     bool marked = false;                          // they are filled
-    bool listed = false;                          // the list holds the range's keys
     if (need > 0) {
         if (hi - lo <= 2 * kSelSample) {
             if (threadIdx.x == 0) sh.range = Range{0u, 0xffffffffu, 0, (int)(hi - lo)};
@@ -343,55 +362,13 @@ __global__ void __launch_bounds__(kSelThreads, 2)
         } else {
             sample_range(sh, list_key, score, lo, hi, need);
         }
-        bool known = hi - lo <= 2 * kSelSample;  // the range's counts are exact
-        // One pass marks and lists; when the range proves wrong or too full, histogram
-        // passes narrow it until the list holds it, or until it is one key.
-        for (;;) {
-            const Range g = sh.range;
-            if (known && g.lo == g.hi) break;
-            if (!known || g.inside <= kSelList) {
-                __syncthreads();
-                if (threadIdx.x == 0) {
-                    sh.listed = 0;
-                    sh.above = 0;
-                }
-                if (one) {
-                    clear_words(above_map, (n + 31) / 32);
-                    clear_words(tie_map, (n + 31) / 32);
-                }
-                __syncthreads();
-                mark_and_list(sh, score, lo, hi, g, one ? above_map : nullptr, list_at);
-                __syncthreads();
-                if (threadIdx.x == 0) {
-                    sh.range.above = sh.above;
-                    sh.range.inside = sh.listed;
-                }
-                __syncthreads();
-                const Range e = sh.range;
-                if (e.above < need && need <= e.above + e.inside) {
-                    known = true;
-                    listed = e.inside <= kSelList;
-                    if (listed) break;
-                } else {  // the sample missed
-                    __syncthreads();
-                    if (threadIdx.x == 0) sh.range = Range{0u, 0xffffffffu, 0, (int)(hi - lo)};
-                    __syncthreads();
-                    known = true;
-                }
-                continue;
-            }
-            clear_words(sh.hist, kSelBins);
-            __syncthreads();
-            const int shift = range_shift(g.lo, g.hi);
-            each_key(score, lo, hi, [&](int64_t, uint32_t key) {
-                if (key >= g.lo && key <= g.hi) count_bin(sh.hist, (int)((key - g.lo) >> shift));
-            });
-            narrow_range(sh, need);
-        }
+        BoundarySearch search{sh,    score, lo,   hi,        need, (int)(hi - lo), (n + 31) / 32,
+                              one ? above_map : nullptr, tie_map, list_at};
+        const bool listed = settle_range(search, hi - lo <= 2 * kSelSample);
         if (listed) {
-            const int m = (int)sh.range.inside;
+            const int m = sh.listed < kSelList ? sh.listed : kSelList;
             for (int i = threadIdx.x; i < m; i += kSelThreads) list_key[i] = score_key(score[list_at[i]]);
-            while (sh.range.lo != sh.range.hi) {
+            for (int pass = 0; pass < kSelPasses && sh.range.lo != sh.range.hi; ++pass) {
                 const Range g = sh.range;
                 __syncthreads();
                 clear_words(sh.hist, kSelBins);
@@ -422,7 +399,9 @@ __global__ void __launch_bounds__(kSelThreads, 2)
     for (int64_t i = threadIdx.x; i < a.first; i += kSelThreads) pos[i] = (int32_t)i;
     for (int64_t i = threadIdx.x; i < a.last; i += kSelThreads)
         pos[a.budget - a.last + i] = (int32_t)(hi + i);
-    // the competitors out of the bit maps, a window of positions at a time
+    // the competitors out of the bit maps, a window of positions at a time; nothing is stored
+    // past their room, not even when the scores change meanwhile
+    const int64_t room = a.budget - a.last;
     int64_t out = a.first, tied = 0;
     for (int64_t w0 = 0; w0 < n; w0 += window) {
         const int64_t w1 = w0 + window < n ? w0 + window : n;
@@ -463,7 +442,8 @@ __global__ void __launch_bounds__(kSelThreads, 2)
                 const int k = __ffs(bits) - 1;
                 bits &= bits - 1;
                 if (((T >> k) & 1u) && left-- <= 0) continue;
-                pos[o++] = (int32_t)(w0 + (int64_t)i * 32 + k);
+                if (o < room) pos[o] = (int32_t)(w0 + (int64_t)i * 32 + k);
+                ++o;
             }
         }
         const int64_t t2 = tied + tot.y;
@@ -493,7 +473,7 @@ __global__ void __launch_bounds__(256)
         const int64_t p = positions[row];
         Pack<T, W> kk, vv;
         float s = 0.f;
-        if (p >= 0) {
+        if (p >= 0 && p < a.N) {  // a place left open by scores that change meanwhile is no position
             kk = *reinterpret_cast<const Pack<T, W>*>(k + b * g.kb + h * g.kh + p * g.kr + c);
             vv = *reinterpret_cast<const Pack<T, W>*>(v + b * g.vb + h * g.vh + p * g.vr + c);
             if (c == 0) s = a.score[b * a.score_b + h * a.score_h + p];
