@@ -359,9 +359,15 @@ RowArgs row_args(int64_t ld, int64_t T, int32_t k, int64_t H, const int32_t* slo
     while ((1 << a.tx) < kRowThreads && ((1 << a.tx) < threads || (1 << a.tx) < least)) ++a.tx;
     return a;
 }
-dim3 row_grid(const RowArgs& a, int per_sm) {
-    const int64_t rows = kRowThreads >> a.tx, want = (a.T + rows - 1) / rows,
-                  most = (int64_t)device_sm_count() * per_sm;
+// Blocks that take every row once (at most T < 2^31 of them), or, for kernels that walk on by
+// row_step, as many as stay busy.
+int64_t row_blocks(const RowArgs& a) {
+    const int64_t rows = kRowThreads >> a.tx;
+    return (a.T + rows - 1) / rows;
+}
+dim3 row_grid(const RowArgs& a) { return dim3((unsigned)row_blocks(a)); }
+dim3 walking_row_grid(const RowArgs& a) {
+    const int64_t want = row_blocks(a), most = (int64_t)device_sm_count() * 16;
     return dim3((unsigned)(want < most ? want : most));
 }
 
@@ -438,7 +444,7 @@ extern "C" int lapsum_expert_gather(const void* x, int dtype, int64_t ld, int64_
         return with_pack<E>(address_bits(x) | address_bits(xs), H, ld, [&](auto w) {
             constexpr int W = decltype(w)::value;
             const RowArgs a = row_args(ld, T, k, H, slots, live, row_threads<E, W>(H), 1);
-            return launch_pdl(expert_gather_kernel<E, W>, row_grid(a, 1 << 20), dim3(kRowThreads), 0, st, a,
+            return launch_pdl(expert_gather_kernel<E, W>, row_grid(a), dim3(kRowThreads), 0, st, a,
                               (const E*)x, (E*)xs);
         });
     });
@@ -461,7 +467,7 @@ extern "C" int lapsum_expert_combine(const void* y, int dtype, int64_t T, int32_
         return with_pack<E>(address_bits(y) | address_bits(out), H, H, [&](auto w) {
             constexpr int W = decltype(w)::value;
             const RowArgs a = row_args(H, T, k, H, slots, live, row_threads<E, W>(H), 1);
-            return launch_pdl(expert_combine_kernel<E, W>, row_grid(a, 16), dim3(kRowThreads), 0, st, a,
+            return launch_pdl(expert_combine_kernel<E, W>, walking_row_grid(a), dim3(kRowThreads), 0, st, a,
                               (const E*)y, weights, (E*)out);
         });
     });
@@ -493,7 +499,7 @@ extern "C" int lapsum_expert_combine_backward(const void* dout, int dtype, int64
                                 const auto go = [&](auto tx) {
                                     return launch_pdl(
                                         expert_combine_backward_kernel<E, W, decltype(tx)::value>,
-                                        row_grid(a, 1 << 20), dim3(kRowThreads), 0, st, a,
+                                        row_grid(a), dim3(kRowThreads), 0, st, a,
                                         (const E*)dout, (const E*)y, weights, (E*)dy, dweights);
                                 };
                                 switch (a.tx) {
