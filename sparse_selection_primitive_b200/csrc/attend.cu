@@ -10,8 +10,8 @@
 // that a few query rows (one token and its G heads) fill a whole instruction, each
 // thread holds one key's logits for all rows, and the column sums that the scores need are
 // sums inside a thread.  O^T = V^T P is D x RT, with V read as it lies.  Weights go to
-// the second product as pairs of 16-bit values, p = hi + lo, so that they keep 16 bits
-// and more of p.  Runs of key tiles are joined by a second kernel; scores come from kept
+// the second product as pairs of 16-bit values, p = hi + lo, which keep 15 bits of p and more
+// (Pair says how small a weight may be).  Runs of key tiles are joined by a second kernel; scores come from kept
 // logits where few rows share a key, and from a second S^T where keeping them would cost more.
 // More than kKeepRows rows a key fill the M side themselves (attend_wide_kernel).
 //
@@ -166,15 +166,26 @@ __device__ __forceinline__ void key_products(uint32_t to, uint64_t k, uint64_t q
     }
 }
 
-// Two weights as words of two 16-bit values each: hi + lo = the weights to 16 bits and more.
+// Two weights as words of two 16-bit values each: p = hi + lo / apart, where `apart` is
+// kApart if the products of hi and lo are summed apart, else 1.
+//
+// A weight is 2^(x - m) for a reference m that keeps the row's largest weight between 2^kLift
+// and 2^kMost.  The bounds of fp16 make the difference.  Its smallest value is 2^-24, and what
+// is below half of that is lost: with lo as it is, up to 2^-25 of a weight, which is 2^-36 of
+// the row's largest one; with lo scaled by kApart, 2^-37 and 2^-48.  A reference at the largest
+// weight itself, with lo as it is, lost all weights below 2^-25 of the largest from the output
+// but not from the sum; with one key that takes nearly all of the weight and has a value near
+// 0, that is most of the output.  2^kMost is half of fp16's largest value, and hi leaves lo at
+// most 2^(kMost - 12), which kApart takes there too.  bf16 has fp32's range.
 template <class T>
 struct Pair;
 template <>
 struct Pair<__nv_bfloat16> {
     static constexpr bool bf16 = true;
+    static constexpr float kLift = 0.f, kMost = 12.f, kApart = 1.f;
     // hi is cut off (a byte permutation; conversions run at a quarter of the rate), which
     // leaves lo up to 2^-7 of the weight; lo is rounded: off by 2^-15 of it at most
-    static __device__ __forceinline__ void split(float a, float b, uint32_t* hi, uint32_t* lo) {
+    static __device__ __forceinline__ void split(float a, float b, float, uint32_t* hi, uint32_t* lo) {
         const uint32_t u = __float_as_uint(a), v = __float_as_uint(b);
         *hi = __byte_perm(u, v, 0x7632);
         const __nv_bfloat162 l =
@@ -185,9 +196,10 @@ struct Pair<__nv_bfloat16> {
 template <>
 struct Pair<__half> {
     static constexpr bool bf16 = false;
-    static __device__ __forceinline__ void split(float a, float b, uint32_t* hi, uint32_t* lo) {
+    static constexpr float kLift = 11.f, kMost = 15.f, kApart = 4096.f;
+    static __device__ __forceinline__ void split(float a, float b, float apart, uint32_t* hi, uint32_t* lo) {
         const __half2 h = __floats2half2_rn(a, b);
-        const __half2 l = __floats2half2_rn(a - __low2float(h), b - __high2float(h));
+        const __half2 l = __floats2half2_rn((a - __low2float(h)) * apart, (b - __high2float(h)) * apart);
         *hi = *reinterpret_cast<const uint32_t*>(&h);
         *lo = *reinterpret_cast<const uint32_t*>(&l);
     }
@@ -198,11 +210,11 @@ struct Pair<__half> {
 // fp32.  Warp 0 loads, warp 1 multiplies, and four warps do the softmax, each on the
 // quarter of the lanes of tensor memory that it can read.
 //
-// Weights are 2^(x - m) with a reference m per row that is the exact maximum of the first
-// tile and is raised only when some logit passes it by kSlack: a maximum over the keys is a
+// Weights are 2^(x - m) with a reference m per row, kLift below the exact maximum of the first
+// tile, that is raised only when some logit passes it by kMost: a maximum over the keys is a
 // maximum across threads, dear to form for every tile, and any reference within a factor
-// 2^kSlack of it serves as well (p <= 2^kSlack stays far inside fp16, and relative errors
-// are the same).  Raising it rescales the sums and the outputs in tensor memory.
+// 2^(kMost - kLift) serves as well.  Raising it rescales the sums and the outputs in tensor
+// memory.
 template <class T>
 __global__ void __launch_bounds__(kNarrowThreads, 2)
     attend_narrow_kernel(AttendArgs a, AttendPlan p, const T* q,
@@ -210,7 +222,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                         const __grid_constant__ CUtensorMap v_map, float2* stats, float* part,
                         float* logits) {
     constexpr int RT = kKeepRows;
-    constexpr float kSlack = 12.f;
+    constexpr float kLift = Pair<T>::kLift, kMost = Pair<T>::kMost, kApart = Pair<T>::kApart;
     extern __shared__ char smem_raw[];
     __shared__ uint64_t bars[2 * kMaxStages + 4];
     __shared__ uint32_t s_tmem;
@@ -414,14 +426,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                     if (key < RT) {
                         const float by = fmaxf(fmaxf(red[0][key], red[1][key]), fmaxf(red[2][key], red[3][key]));
                         unseen = !s_seen[key] && by == -INFINITY;
-                        const float up = unseen ? 0.f : s_seen[key] ? fmaxf(by, 0.f) : by;
+                        const float up = unseen ? 0.f : s_seen[key] ? fmaxf(by - kLift, 0.f) : by - kLift;
                         s_ref[key] += up;
                         s_up[key] = up;
                         s_scale[key] = s_seen[key] ? ex2_ftz(-up) : 0.f;
                         s_seen[key] = !unseen;
                     }
                     unseen = __any_sync(kAll, unseen);
-                    if (key == 0) s_slack = unseen ? -INFINITY : kSlack;
+                    if (key == 0) s_slack = unseen ? -INFINITY : kMost;
                 }
                 softmax_sync<128>();
 #pragma unroll
@@ -461,7 +473,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    Pair<T>::split(x[r + 2 * i], x[r + 2 * i + 1], &hi[i], &lo[i]);
+                    Pair<T>::split(x[r + 2 * i], x[r + 2 * i + 1], kApart, &hi[i], &lo[i]);
                 const uint32_t to = p_at + (r >> 3) * 2048 + key * 16;
                 asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(hi[0]),
                              "r"(hi[1]), "r"(hi[2]), "r"(hi[3])
@@ -498,7 +510,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                 if (d < a.D)
 #pragma unroll
                     for (int r = 0; r < RT; ++r)
-                        if (r < rows) to[(int64_t)r * a.D] = o[r] + lo[r];
+                        if (r < rows) to[(int64_t)r * a.D] = fmaf(lo[r], 1.f / kApart, o[r]);
             }
         tc_fence_before();
     }
@@ -522,7 +534,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                        const __grid_constant__ CUtensorMap k_map,
                        const __grid_constant__ CUtensorMap v_map, float2* stats, float* part) {
     constexpr int RT = 128, kHalf = kTile / 2;
-    constexpr float kSlack = 12.f;
+    constexpr float kLift = Pair<T>::kLift, kMost = Pair<T>::kMost, kApart = Pair<T>::kApart;
     extern __shared__ char smem_raw[];
     __shared__ uint64_t bars[2 * kMaxStages + 5];
     __shared__ uint32_t s_tmem;
@@ -577,8 +589,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // logits (then weights) of two tiles, then the outputs
+    // logits (then weights) of two tiles, then the outputs; where there is room for two (and for
+    // fp16 only), those of the weights' hi and lo parts apart
     const uint32_t tmem = uniform(s_tmem), o_col = tmem + 2 * kTile;
+    const bool two = kApart != 1.f && a.D <= 128;
+    const uint32_t lo_col = two ? 128 : 0;
+    const float apart = two ? kApart : 1.f;
     // the ring's items: K0, K1, V0, K2, V1, ..., V(last)
     const int items = 2 * tiles;
     auto key_item = [](int t) { return t == 0 ? 0 : 2 * t - 1; };
@@ -639,7 +655,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 for (int kk = 0; kk < kTile / 16; ++kk) {
                     const uint32_t w = tmem + (t & 1) * kTile + (kk >> 2) * kHalf + (kk & 3) * 8;
                     mma_f16_ta(o_col, w, v + advance(kk * 2048), shape_o, t + kk > 0);
-                    mma_f16_ta(o_col, w + 32, v + advance(kk * 2048), shape_o, true);
+                    mma_f16_ta(o_col + lo_col, w + 32, v + advance(kk * 2048), shape_o, !two || t + kk > 0);
                 }
                 mma_commit(empty + 8 * s);
                 mma_commit(p_used);
@@ -703,7 +719,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     "{\n\t.reg .pred u, v;\n\tsetp.ne.u32 u, %1, 0;\n\t"
                     "barrier.cta.red.or.pred v, %2, 64, u;\n\tselp.u32 %0, 1, 0, v;\n\t}"
                     : "=r"(raise)
-                    : "r"(by > (fresh ? -INFINITY : kSlack) ? 1u : 0u), "r"(2 + quarter)
+                    : "r"(by > (fresh ? -INFINITY : kMost) ? 1u : 0u), "r"(2 + quarter)
                     : "memory");
                 if (raise) {
                     s_pair[half][row] = by;
@@ -716,7 +732,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     const float both = fmaxf(s_pair[0][row], s_pair[1][row]);
                     asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory");
                     const bool none = fresh && both == -INFINITY;
-                    const float up = none ? 0.f : fresh ? both : fmaxf(both, 0.f);
+                    const float up = none ? 0.f : fresh ? both - kLift : fmaxf(both - kLift, 0.f);
                     const float scale = fresh ? 0.f : ex2_ftz(-up);
                     ref += up;
                     fresh = none;
@@ -724,13 +740,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
                     for (int c = 0; c < kHalf; ++c) x[c] -= up;
                     if (t > 0)  // each thread rescales half of the row's outputs
-                        for (int c = half * 16; c < a.D; c += 32) {
-                            float o[16];
-                            tmem_ld<16>(lanes + 2 * kTile + c, o);
+                        for (uint32_t col = 0; col <= lo_col; col += 128)
+                            for (int c = half * 16; c < a.D; c += 32) {
+                                float o[16];
+                                tmem_ld<16>(lanes + 2 * kTile + col + c, o);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] *= scale;
-                            tmem_st<16>(lanes + 2 * kTile + c, o);
-                        }
+                                for (int i = 0; i < 16; ++i) o[i] *= scale;
+                                tmem_st<16>(lanes + 2 * kTile + col + c, o);
+                            }
                 }
                 float part_sum[4] = {0.f, 0.f, 0.f, 0.f};
                 uint32_t hi[kHalf / 2], lo[kHalf / 2];
@@ -739,7 +756,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     const float u = ex2_ftz(x[c]), w = ex2_ftz(x[c + 1]);
                     part_sum[c & 3] += u;
                     part_sum[(c & 3) + 1] += w;
-                    Pair<T>::split(u, w, &hi[c / 2], &lo[c / 2]);
+                    Pair<T>::split(u, w, apart, &hi[c / 2], &lo[c / 2]);
                 }
                 sum += (part_sum[0] + part_sum[1]) + (part_sum[2] + part_sum[3]);
                 tmem_st<32>(at, hi);
@@ -768,6 +785,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             for (int c = half * 16; c < a.D; c += 32) {
                 float o[16];
                 tmem_ld<16>(lanes + 2 * kTile + c, o);
+                if (two) {
+                    float lo[16];
+                    tmem_ld<16>(lanes + 2 * kTile + lo_col + c, lo);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = fmaf(lo[i], 1.f / kApart, o[i]);
+                }
                 if (row < rows)
 #pragma unroll
                     for (int i = 0; i < 16; i += 4)
