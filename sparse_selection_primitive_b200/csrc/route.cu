@@ -446,9 +446,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     if constexpr (kKeyed) {
         bool close = false;  // two neighbouring ranks that fp32 does not tell apart
         if (check) {
-            const uint32_t next = __shfl_down_sync(kAll, mine, 1);
-            close = lane < a.k && (lane == 31 || (mine != 0u && next != 0u &&
-                                                  from_key(mine) - from_key(next) <= 2.f * tol));
+            uint32_t next = __shfl_down_sync(kAll, mine, 1);
+            if (a.k == 32) {  // no lane holds the key after the last one: the largest that is left
+                uint32_t left = 0;
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (found == 0 || key[i] < reach) left = max(left, key[i]);
+                reach = __reduce_max_sync(kAll, left);
+                if (lane == 31) next = reach;
+            }
+            close = lane < a.k && mine != 0u && next != 0u &&
+                    from_key(mine) - from_key(next) <= 2.f * tol;
             close = __any_sync(kAll, close);
         }
         near = __any_sync(kAll, near);  // or two groups
@@ -456,8 +464,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
             // all that may belong to the first k are among the candidates when those reach
             // further than the error below the k-th
             const uint32_t kth = __shfl_sync(kAll, mine, a.k - 1);
-            if (found > 0 && a.k < 32 && (kth == 0u || reach <= 1u ||
-                                          from_key(kth) - 2.f * tol > from_key(reach)))
+            if (found > 0 && (kth == 0u || reach <= 1u ||
+                              from_key(kth) - 2.f * tol > from_key(reach)))
                 chosen = rank_fp64<T>(row, a, lane, chosen, found);
             else
                 near = true;
