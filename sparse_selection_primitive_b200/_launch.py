@@ -3,6 +3,7 @@ and the checks of tensor arguments."""
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad
 
 from . import LapSumError
 
@@ -66,6 +67,15 @@ def distinct(x: torch.Tensor) -> bool:
             return False
         need_stride = s * (n - 1) + need_stride
     return True
+
+
+def no_tangents(name: str, *tensors):
+    """Refuses forward-mode inputs: the library reads their values and would drop their
+    tangents unnoticed."""
+    if forward_ad._current_level < 0:  # no dual tensors outside a level (unpack_dual's own test)
+        return
+    if any(forward_ad.unpack_dual(x).tangent is not None for x in tensors):
+        raise NotImplementedError(f"{name} has no forward-mode derivative")
 
 
 def no_gradient(name: str):

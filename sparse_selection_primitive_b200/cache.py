@@ -15,7 +15,8 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
-from ._launch import DTYPES, distinct, extent, launch, need, no_gradient, overlap
+from ._launch import (DTYPES, distinct, extent, launch, need, no_gradient, no_tangents,
+                      overlap)
 
 _HALF = (torch.bfloat16, torch.float16)
 _F32, _I32 = (torch.float32,), (torch.int32,)
@@ -61,6 +62,7 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
     _, Hkv, N, _ = k.shape
     if q.requires_grad or k.requires_grad or v.requires_grad or score.requires_grad:
         no_gradient("attend_accumulate")
+    no_tangents("attend_accumulate", q, k, v, score)
     qs = q.stride()
     if B != k.shape[0] or D != k.shape[3] or Hkv < 1 or Hq % Hkv != 0:
         raise ValueError("q must be (B, Sq, Hq, D) with Hq a multiple of the caches' heads")
@@ -126,6 +128,7 @@ def evict(k: torch.Tensor, v: torch.Tensor, score: torch.Tensor, lengths: torch.
     ks, vs, ss = _check_caches(k, v, score, lengths, DTYPES)
     if k.requires_grad or v.requires_grad or score.requires_grad:
         no_gradient("evict")
+    no_tangents("evict", k, v, score)
     B, H, N, D = k.shape
     budget, first, last = int(budget), int(first), int(last)
     if budget < 1 or first < 0 or last < 0 or first + last > budget:

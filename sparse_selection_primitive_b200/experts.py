@@ -15,7 +15,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from ._launch import DTYPES, launch, need
+from ._launch import DTYPES, launch, need, no_tangents
 
 SCORES = {"softmax": 0, "sigmoid": 1}
 
@@ -56,6 +56,7 @@ def route_backward(logits: torch.Tensor, weights: torch.Tensor, experts: torch.T
         raise ValueError("weights, experts and dweights must be (rows of logits) x k")
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
+    no_tangents("route_backward", logits, weights, dweights)
     return _route_grad(_rows(logits), weights.contiguous(), experts.contiguous(),
                        dweights.contiguous(), SCORES[score], bool(renormalize), float(scale))
 
@@ -125,6 +126,7 @@ def route_experts(logits: torch.Tensor, k: int, *, score: str = "softmax", bias=
         if bias.shape[0] != logits.shape[1]:
             raise ValueError("bias must have one entry per expert")
         bias = bias.detach().contiguous()
+    no_tangents("route_experts", logits)
     logits = _rows(logits)
     renormalize, scale = bool(renormalize), float(scale)
     run = _Route.apply if logits.requires_grad and torch.is_grad_enabled() else _route
@@ -212,6 +214,7 @@ def expert_gather(x: torch.Tensor, plan: ExpertPlan) -> torch.Tensor:
     _check_plan(plan, x.device)
     if x.shape[0] != plan.slots.shape[0]:
         raise ValueError("x must have one row per row of the plan")
+    no_tangents("expert_gather", x)
     x = _rows(x)
     if x.requires_grad and torch.is_grad_enabled():
         return _Gather.apply(x, *plan)
@@ -252,6 +255,7 @@ def expert_combine(y: torch.Tensor, weights: torch.Tensor, plan: ExpertPlan) -> 
         raise ValueError("weights must have the shape of plan.slots")
     if y.shape[0] != plan.slots.numel():
         raise ValueError("y must have one row per assignment of the plan")
+    no_tangents("expert_combine", y, weights)
     y, weights = y.contiguous(), weights.contiguous()
     if torch.is_grad_enabled() and (y.requires_grad or weights.requires_grad):
         return _Combine.apply(y, weights, plan.offsets, plan.slots)
