@@ -7,22 +7,22 @@ from torch.autograd import forward_ad
 
 from . import LapSumError
 
-# the calls behind torch.cuda.current_device and current_stream, without building a Stream
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
 def launch(fn, device, *args):
     """Calls the library function with the current stream of ``device`` as its last
-    argument, on that device whatever the current one is; raises on an error."""
-    index = device.index
-    if index == _current_device():
-        code = fn(*args, _raw_stream(index))
+    argument, on that device whatever the current one is; raises on an error.
+
+    The device and the stream come from the calls behind torch.cuda.current_device and
+    current_stream, which build no Stream; a torch without CUDA does not have them, and the
+    package has to be imported there too."""
+    index, stream = device.index, torch._C._cuda_getCurrentRawStream
+    if index == torch._C._cuda_getDevice():
+        code = fn(*args, stream(index))
     else:
         with torch.cuda.device(index):
-            code = fn(*args, _raw_stream(index))
+            code = fn(*args, stream(index))
     if code != 0:
         raise LapSumError(code, fn.__name__)
 

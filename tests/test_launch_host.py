@@ -1,9 +1,13 @@
 """The checks of tensor arguments that the expert and cache calls share, on the host."""
+import subprocess
+import sys
+
 import pytest
 import torch
 import torch.autograd.forward_ad as fw
 
 from sparse_selection_primitive_b200 import _launch
+from tests.conftest import ROOT
 
 
 def test_tangents_are_refused():
@@ -23,3 +27,14 @@ def test_tangents_are_refused():
 
     with pytest.raises(NotImplementedError):
         torch.func.jvp(inner, (x,), (torch.ones(3),))
+
+
+def test_import_without_cuda():
+    """The package and its host-side parts are imported with a torch that was built without CUDA,
+    which has none of the device calls."""
+    code = ("import torch\n"
+            "for name in [n for n in dir(torch._C) if n.startswith('_cuda_get')]:\n"
+            "    delattr(torch._C, name)\n"
+            "import sparse_selection_primitive_b200\n"
+            "import sparse_selection_primitive_b200.sharded\n")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT)
