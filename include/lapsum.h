@@ -497,6 +497,8 @@ int lapsum_route_backward(const void* logits, int dtype, int64_t ld, int64_t T, 
  *     weights NULL: ones, which makes it the gradient of lapsum_expert_gather.
  *   lapsum_expert_combine_backward:  dy[slots[t*k+j]] = weights[t*k+j] dout[t] and
  *     dweights[t*k+j] = dout[t] . y[slots[t*k+j]]; 0 for dropped assignments.
+ *   lapsum_expert_combine_backward_part:  the same with dy or dweights NULL (not both), which
+ *     is then not formed; y is not read, and may be NULL, without dweights.
  * A slot outside [0, N) is skipped.  No result depends on the order of execution.
  */
 size_t lapsum_expert_plan_workspace_bytes(int64_t N, int64_t E);
@@ -511,6 +513,10 @@ int lapsum_expert_combine_backward(const void* dout, int dtype, int64_t ld, cons
                                    int64_t T, int32_t k, int64_t H, const int32_t* slots,
                                    const int32_t* live, const float* weights, void* dy,
                                    float* dweights, void* stream);
+int lapsum_expert_combine_backward_part(const void* dout, int dtype, int64_t ld, const void* y,
+                                        int64_t T, int32_t k, int64_t H, const int32_t* slots,
+                                        const int32_t* live, const float* weights, void* dy,
+                                        float* dweights, void* stream);
 
 /*
  * Attention over a cache with accumulated weight.  Sq tokens of each of B

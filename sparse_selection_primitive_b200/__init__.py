@@ -171,6 +171,9 @@ def _lib():
         lib.lapsum_expert_combine_backward.restype = ctypes.c_int
         lib.lapsum_expert_combine_backward.argtypes = [_vp, ctypes.c_int, _c_i64, _vp, _c_i64, i32,
                                                        _c_i64, _vp, _vp, _vp, _vp, _vp, _vp]
+        lib.lapsum_expert_combine_backward_part.restype = ctypes.c_int
+        lib.lapsum_expert_combine_backward_part.argtypes = \
+            lib.lapsum_expert_combine_backward.argtypes
         lib.lapsum_attend_workspace_bytes.restype = ctypes.c_size_t
         lib.lapsum_attend_workspace_bytes.argtypes = [_c_i64] * 6
         lib.lapsum_attend_accumulate.restype = ctypes.c_int

@@ -1,6 +1,6 @@
 // Rows of a batch moved to their experts and back.  Entry points:
 // lapsum_expert_plan, lapsum_expert_gather, lapsum_expert_combine,
-// lapsum_expert_combine_backward (include/lapsum.h).
+// lapsum_expert_combine_backward, lapsum_expert_combine_backward_part (include/lapsum.h).
 //
 // The plan is a stable counting sort of the T k assignments by expert, with the
 // dropped ones (no expert) behind the last expert, so that `slots` is always a
@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(kRowThreads, 8)
 // dropped assignments.  TX is 32 at least, so that whole warps share a row's products, and
 // known to the compiler, which then unrolls the walk along the row: 197 us instead of 247 for
 // 16384 x 8 rows of 4 KB, 189 instead of 388 for rows of 2049 16-bit elements (half as many).
-template <class T, int W, int TX>
+// kDy, kDw: which of the two is formed; without dw y is not read.
+template <class T, int W, int TX, bool kDy, bool kDw>
 __global__ void __launch_bounds__(kRowThreads)
     expert_combine_backward_kernel(RowArgs a, const T* dout, const T* y, const float* w, T* dy,
                                    float* dw) {
@@ -306,24 +307,28 @@ __global__ void __launch_bounds__(kRowThreads)
                     Pack<T, W> o;
                     if (on) {
                         const Pack<T, W> g = *reinterpret_cast<const Pack<T, W>*>(dout + t * a.ld + c);
-                        const Pack<T, W> v = *reinterpret_cast<const Pack<T, W>*>(y + (int64_t)s * a.H + c);
+                        Pack<T, W> v;
+                        if constexpr (kDw) v = *reinterpret_cast<const Pack<T, W>*>(y + (int64_t)s * a.H + c);
 #pragma unroll
                         for (int q = 0; q < W; ++q) {
-                            dot = fmaf(widen(g.v[q]), widen(v.v[q]), dot);
+                            if constexpr (kDw) dot = fmaf(widen(g.v[q]), widen(v.v[q]), dot);
                             o.v[q] = narrow<T>(wj * widen(g.v[q]));
                         }
                     } else {
 #pragma unroll
                         for (int q = 0; q < W; ++q) o.v[q] = narrow<T>(0.f);
                     }
-                    *reinterpret_cast<Pack<T, W>*>(dy + (int64_t)s * a.H + c) = o;
+                    if constexpr (kDy) *reinterpret_cast<Pack<T, W>*>(dy + (int64_t)s * a.H + c) = o;
                 }
             }
+            if constexpr (kDw) {
 #pragma unroll
-            for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(kAll, dot, d);
-            if (lane == 0) part[warp][j] = dot;
+                for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(kAll, dot, d);
+                if (lane == 0) part[warp][j] = dot;
+            }
         }
     }
+    if constexpr (!kDw) return;
     __syncthreads();
     if (t < a.T && at < a.k) {  // thread j of a row adds up its warps' parts
         const int w0 = threadIdx.x / TX * (TX / 32);
@@ -474,13 +479,13 @@ extern "C" int lapsum_expert_combine(const void* y, int dtype, int64_t T, int32_
     return e == cudaSuccess ? LAPSUM_OK : LAPSUM_ECUDA;
 }
 
-extern "C" int lapsum_expert_combine_backward(const void* dout, int dtype, int64_t ld,
-                                              const void* y, int64_t T, int32_t k, int64_t H,
-                                              const int32_t* slots, const int32_t* live,
-                                              const float* weights, void* dy, float* dweights,
-                                              void* stream) {
-    if (dout == nullptr || y == nullptr || slots == nullptr || live == nullptr ||
-        weights == nullptr || dy == nullptr || dweights == nullptr)
+namespace {
+
+int combine_backward(const void* dout, int dtype, int64_t ld, const void* y, int64_t T, int32_t k,
+                     int64_t H, const int32_t* slots, const int32_t* live, const float* weights,
+                     void* dy, float* dweights, void* stream) {
+    if (dout == nullptr || slots == nullptr || live == nullptr || weights == nullptr ||
+        (y == nullptr && dweights != nullptr) || (dy == nullptr && dweights == nullptr))
         return LAPSUM_EINVAL;
     if (!known_dtype(dtype) || !rows_ok(T, k, H) || ld < H) return LAPSUM_EINVAL;
     const int size = dtype_size(dtype);
@@ -492,23 +497,45 @@ extern "C" int lapsum_expert_combine_backward(const void* dout, int dtype, int64
     ProfScope prof("expert_combine_backward", st);
     const cudaError_t e = with_dtype(dtype, [&](auto* tag) {
         using E = std::remove_const_t<std::remove_pointer_t<decltype(tag)>>;
-        return with_pack<E>(address_bits(dout) | address_bits(y) | address_bits(dy), H, ld,
-                            [&](auto w) {
-                                constexpr int W = decltype(w)::value;
-                                const RowArgs a = row_args(ld, T, k, H, slots, live, H / W, 32);
-                                const auto go = [&](auto tx) {
-                                    return launch_pdl(
-                                        expert_combine_backward_kernel<E, W, decltype(tx)::value>,
-                                        row_grid(a), dim3(kRowThreads), 0, st, a,
-                                        (const E*)dout, (const E*)y, weights, (E*)dy, dweights);
-                                };
-                                switch (a.tx) {
-                                    case 5: return go(std::integral_constant<int, 32>{});
-                                    case 6: return go(std::integral_constant<int, 64>{});
-                                    case 7: return go(std::integral_constant<int, 128>{});
-                                    default: return go(std::integral_constant<int, 256>{});
-                                }
-                            });
+        return with_pack<E>(address_bits(dout) | address_bits(y) | address_bits(dy), H, ld, [&](auto w) {
+            constexpr int W = decltype(w)::value;
+            const RowArgs a = row_args(ld, T, k, H, slots, live, H / W, 32);
+            const auto go = [&](auto tx) {
+                constexpr int TX = decltype(tx)::value;
+                const auto run = [&](auto kernel) {
+                    return launch_pdl(kernel, row_grid(a), dim3(kRowThreads), 0, st, a, (const E*)dout,
+                                      (const E*)y, weights, (E*)dy, dweights);
+                };
+                if (dweights == nullptr) return run(expert_combine_backward_kernel<E, W, TX, true, false>);
+                if (dy == nullptr) return run(expert_combine_backward_kernel<E, W, TX, false, true>);
+                return run(expert_combine_backward_kernel<E, W, TX, true, true>);
+            };
+            switch (a.tx) {
+                case 5: return go(std::integral_constant<int, 32>{});
+                case 6: return go(std::integral_constant<int, 64>{});
+                case 7: return go(std::integral_constant<int, 128>{});
+                default: return go(std::integral_constant<int, 256>{});
+            }
+        });
     });
     return e == cudaSuccess ? LAPSUM_OK : LAPSUM_ECUDA;
+}
+
+}  // namespace
+
+extern "C" int lapsum_expert_combine_backward(const void* dout, int dtype, int64_t ld,
+                                              const void* y, int64_t T, int32_t k, int64_t H,
+                                              const int32_t* slots, const int32_t* live,
+                                              const float* weights, void* dy, float* dweights,
+                                              void* stream) {
+    if (y == nullptr || dy == nullptr || dweights == nullptr) return LAPSUM_EINVAL;
+    return combine_backward(dout, dtype, ld, y, T, k, H, slots, live, weights, dy, dweights, stream);
+}
+
+extern "C" int lapsum_expert_combine_backward_part(const void* dout, int dtype, int64_t ld,
+                                                   const void* y, int64_t T, int32_t k, int64_t H,
+                                                   const int32_t* slots, const int32_t* live,
+                                                   const float* weights, void* dy, float* dweights,
+                                                   void* stream) {
+    return combine_backward(dout, dtype, ld, y, T, k, H, slots, live, weights, dy, dweights, stream);
 }

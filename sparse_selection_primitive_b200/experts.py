@@ -224,7 +224,9 @@ def expert_gather(x: torch.Tensor, plan: ExpertPlan) -> torch.Tensor:
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, offsets, slots):
-        ctx.save_for_backward(y, weights, offsets, slots)
+        # y is needed for the weights' gradient only
+        ctx.save_for_backward(y if ctx.needs_input_grad[1] else None, weights, offsets, slots)
+        ctx.rows = y.shape
         return _combine(y, weights, ExpertPlan(offsets, slots, None))
 
     @_once
@@ -232,14 +234,15 @@ class _Combine(torch.autograd.Function):
         y, weights, offsets, slots = ctx.saved_tensors
         plan = ExpertPlan(offsets, slots, None)
         dout = _rows(dout)
-        (T, k), H = slots.shape, y.shape[1]
-        dy = torch.empty_like(y)
-        dw = torch.empty_like(weights)
-        if y.numel() == 0:
-            return dy, dw.zero_(), None, None
-        launch(_lib().lapsum_expert_combine_backward, y.device, dout.data_ptr(), DTYPES[y.dtype],
-               _ld(dout), y.data_ptr(), T, k, H, slots.data_ptr(), plan.live, weights.data_ptr(),
-               dy.data_ptr(), dw.data_ptr())
+        (T, k), H = slots.shape, dout.shape[1]
+        dy = dout.new_empty(ctx.rows) if ctx.needs_input_grad[0] else None
+        dw = torch.empty_like(weights) if ctx.needs_input_grad[1] else None
+        if ctx.rows.numel() == 0:
+            return dy, None if dw is None else dw.zero_(), None, None
+        ptr = lambda x: None if x is None else x.data_ptr()  # noqa: E731
+        launch(_lib().lapsum_expert_combine_backward_part, dout.device, dout.data_ptr(),
+               DTYPES[dout.dtype], _ld(dout), ptr(y), T, k, H, slots.data_ptr(), plan.live,
+               weights.data_ptr(), ptr(dy), ptr(dw))
         return dy, dw, None, None
 
 

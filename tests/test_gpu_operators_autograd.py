@@ -52,3 +52,57 @@ def test_jvp_is_refused(cuda_device):
         which, x = next(iter(inputs.items()))
         with pytest.raises(RuntimeError):
             torch.func.jvp(lambda t: call(**{**inputs, which: t}), (x,), (torch.ones_like(x),))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,k,H", [(9, 3, 40), (300, 8, 257), (70, 2, 2048), (1, 1, 1)])
+def test_combination_forms_the_gradients_that_are_asked_for(cuda_device, dtype, T, k, H):
+    """One of the two alone has the bits that it has beside the other."""
+    gen = torch.Generator().manual_seed(T + H)
+    experts = torch.randint(-1, 5, (T, k), generator=gen).to(torch.int32).cuda()
+    plan = L.expert_plan(experts, 5)
+    y0 = torch.randn((T * k, H), generator=gen).to(dtype).cuda()
+    w0 = torch.rand((T, k), generator=gen).cuda()
+    dout = torch.randn((T, H), generator=gen).to(dtype).cuda()
+
+    def grads(wants_y, wants_w):
+        y, w = y0.clone().requires_grad_(wants_y), w0.clone().requires_grad_(wants_w)
+        out = L.expert_combine(y, w, plan)
+        if not wants_w:
+            y.detach().fill_(float("nan"))  # not kept, not read
+        return torch.autograd.grad(out, [x for x in (y, w) if x.requires_grad], dout)
+
+    dy, dw = grads(True, True)
+    only_y, = grads(True, False)
+    only_w, = grads(False, True)
+    assert torch.equal(only_y, dy) and torch.equal(only_w, dw)
+    # asked for one of two
+    y, w = y0.clone().requires_grad_(True), w0.clone().requires_grad_(True)
+    out = L.expert_combine(y, w, plan)
+    assert torch.equal(torch.autograd.grad(out, y, dout, retain_graph=True)[0], dy)
+    assert torch.equal(torch.autograd.grad(out, w, dout)[0], dw)
+
+
+def test_combination_takes_no_memory_for_other_gradients(cuda_device):
+    T, k, H = 4096, 8, 1024
+    plan = L.expert_plan(torch.randint(0, 16, (T, k), dtype=torch.int32, device="cuda"), 16)
+    w0, dout = torch.rand((T, k), device="cuda"), torch.randn((T, H), device="cuda")
+    rows = T * k * H * 4
+
+    def peak(wants_y, wants_w):
+        y = torch.randn((T * k, H), device="cuda").requires_grad_(wants_y)
+        w = w0.clone().requires_grad_(wants_w)
+        out = L.expert_combine(y, w, plan)
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        torch.autograd.grad(out, y if wants_y else w, dout)
+        return torch.cuda.max_memory_allocated() - before
+
+    assert peak(True, False) >= rows
+    assert peak(False, True) < rows / 8
+    # a temporary y is not kept for the weights of a fixed router
+    leaf = torch.randn((1, H), device="cuda", requires_grad=True)
+    before = torch.cuda.memory_allocated()
+    out = L.expert_combine(leaf.expand(T * k, H) * 1.0, w0, plan)
+    assert torch.cuda.memory_allocated() - before < rows / 2
+    assert out.grad_fn is not None
