@@ -386,12 +386,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 2)
                     if (at >= s_lim[r]) x[r] = -INFINITY;
             }
             if (j < n) {
+                // the rows of zeros past the last one have NaN where a key is infinite: 0 there
                 float* to = logits + (bh * a.N + j) * p.RP + row0;
 #pragma unroll
                 for (int r = 0; r < RT; r += 4)
                     if (row0 + r < p.RP)
                         *reinterpret_cast<float4*>(to + r) =
-                            make_float4(x[r], x[r + 1], x[r + 2], x[r + 3]);
+                            make_float4(x[r], r + 1 < rows ? x[r + 1] : 0.f, r + 2 < rows ? x[r + 2] : 0.f,
+                                        r + 3 < rows ? x[r + 3] : 0.f);
             }
             float over[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -1064,10 +1066,14 @@ __global__ void __launch_bounds__(kScoreThreads, 2)
                     for (int c = 0; c < rows; c += 32) {
                         float x[32];
                         tmem_ld<32>(lanes + c, x);
-                        if (__any_sync(kAll, from > c)) {
+                        // rows that do not see the key, and those of zeros past the last one (whose
+                        // product with an infinite key is NaN), count nothing
+                        if (__any_sync(kAll, from > c) || c + 32 > rows) {
 #pragma unroll
                             for (int r = 0; r < 32; ++r)
-                                s += c + r >= from ? ex2_ftz(fmaf(x[r], a.scale_log2, -s_log[c + r])) : 0.f;
+                                s += c + r >= from && c + r < rows
+                                         ? ex2_ftz(fmaf(x[r], a.scale_log2, -s_log[c + r]))
+                                         : 0.f;
                         } else {
 #pragma unroll
                             for (int r = 0; r < 32; ++r)
