@@ -172,6 +172,8 @@ def _check_plan(plan: ExpertPlan, device):
     need(plan.slots, "plan.slots", (torch.int32,), 2, device)
     if not plan.slots.is_contiguous() or not plan.offsets.is_contiguous():
         raise ValueError("the plan's tensors must be contiguous")
+    if plan.offsets.shape[0] < 2:  # the last entry is read
+        raise ValueError("plan.offsets must have one entry more than there are experts")
 
 
 def _gather(x, plan):
