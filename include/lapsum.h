@@ -558,7 +558,7 @@ int lapsum_attend_accumulate(const void* q, const void* k, const void* v, int dt
  * `dtype`.  `strides` (host, 16 entries, in elements): batch, head and row stride
  * of k, then of v; batch and head stride of score; the same eight of k_out,
  * v_out and score_out (not read for dimensions of one element).  The outputs must not
- * overlap the inputs.  first + last <= budget.
+ * overlap the inputs or each other.  first + last <= budget.
  */
 int lapsum_evict(const void* k, const void* v, int dtype, const float* score,
                  const int32_t* lengths, const int64_t* strides, int64_t B, int64_t H, int64_t N,

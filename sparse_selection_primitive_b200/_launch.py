@@ -57,6 +57,33 @@ def overlap(x: torch.Tensor, y: torch.Tensor) -> bool:
     return a[0] < b[1] and b[0] < a[1]
 
 
+def apart(x: torch.Tensor, y: torch.Tensor) -> bool:
+    """Whether x and y are known to share no memory: their extents do not overlap, or they lie
+    side by side in one structure (the same steps in their first dimensions, and inside one
+    step parts that do not overlap and together are no longer than it)."""
+    if not overlap(x, y):
+        return True
+    steps = []
+    for d in range(min(x.dim(), y.dim()) - 1):
+        if x.shape[d] != y.shape[d]:
+            break
+        if x.shape[d] > 1:
+            step = x.stride(d) * x.element_size()
+            if step != y.stride(d) * y.element_size():
+                break
+            steps.append((step, x.shape[d]))
+        (a0, a1), (b0, b1) = extent(x[(0,) * (d + 1)]), extent(y[(0,) * (d + 1)])
+        if a1 <= b0 or b1 <= a0:
+            span = max(a1, b1) - min(a0, b0)
+            for step, n in sorted(steps):
+                if step < span:
+                    break
+                span += step * (n - 1)
+            else:
+                return True
+    return False
+
+
 def distinct(x: torch.Tensor) -> bool:
     """Whether no two of x's elements share memory (strides nest without overlap)."""
     if x.is_contiguous():

@@ -15,8 +15,7 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
-from ._launch import (DTYPES, distinct, extent, launch, need, no_gradient, no_tangents,
-                      overlap)
+from ._launch import DTYPES, apart, distinct, launch, need, no_gradient, no_tangents, overlap
 
 _HALF = (torch.bfloat16, torch.float16)
 _F32, _I32 = (torch.float32,), (torch.int32,)
@@ -123,7 +122,8 @@ def evict(k: torch.Tensor, v: torch.Tensor, score: torch.Tensor, lengths: torch.
     (B, H, N, float32; ties: the lower position), in the order of their positions.
 
     ``out`` may hold the caches and scores to fill, (k, v, score) with at least
-    ``budget`` rows; rows from ``budget`` on are left as they were.  Rows that no key
+    ``budget`` rows, that share no memory with the inputs or with each other (k and v may lie
+    side by side in one tensor); rows from ``budget`` on are left as they were.  Rows that no key
     fills (fewer than ``budget`` in the cache) are 0 and their positions -1."""
     ks, vs, ss = _check_caches(k, v, score, lengths, DTYPES)
     if k.requires_grad or v.requires_grad or score.requires_grad:
@@ -147,9 +147,11 @@ def evict(k: torch.Tensor, v: torch.Tensor, score: torch.Tensor, lengths: torch.
                     x.shape[-1] > 1 and x.stride(-1) != 1 or not distinct(x):
                 raise ValueError("out must be (B, H, C, D), (B, H, C, D) and (B, H, C) with "
                                  "C >= budget, consecutive in the last dimension")
-        if any(overlap(x, y) for x in (ko, vo, so) for y in (k, v, score, lengths)) or \
-                extent(ko) == extent(vo):
+        if any(overlap(x, y) for x in (ko, vo, so) for y in (k, v, score, lengths)):
             raise ValueError("out must not overlap the inputs")
+        kw, vw, sw = (x[:, :, :budget] for x in (ko, vo, so))  # what is written
+        if not (apart(kw, vw) and apart(kw, sw) and apart(vw, sw)):
+            raise ValueError("the tensors of out must not share memory")
     positions = lengths.new_empty((B, H, budget))
     left = torch.empty_like(lengths)
     result = Evicted(ko, vo, so, positions, left)
