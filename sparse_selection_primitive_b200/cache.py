@@ -13,6 +13,7 @@ import functools
 from typing import NamedTuple
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from ._launch import DTYPES, apart, distinct, launch, need, no_gradient, no_tangents, overlap
@@ -79,9 +80,11 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
             raise ValueError("score_out must be score itself or not overlap it")
     if not distinct(score_out):
         raise ValueError("the scores written must not share memory")
+    written = score_out
     if out is None:
         out = q.new_empty(q.shape)
     else:
+        written = score_out, out
         need(out, "out", (q.dtype,), 4, q.device)
         if out.shape != q.shape or not out.is_contiguous():
             raise ValueError("out must be contiguous and have q's shape")
@@ -101,6 +104,7 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
            DTYPES[q.dtype], lengths.data_ptr(), strides, B, Sq, Hq, Hkv, N, D,
            D ** -0.5 if scale is None else float(scale), score.data_ptr(), score_out.data_ptr(),
            out.data_ptr(), ws.data_ptr(), nbytes)
+    increment_version(written)  # a graph that kept their values has to see that they changed
     return out
 
 
@@ -165,4 +169,6 @@ def evict(k: torch.Tensor, v: torch.Tensor, score: torch.Tensor, lengths: torch.
     launch(_lib().lapsum_evict, k.device, k.data_ptr(), v.data_ptr(), DTYPES[k.dtype],
            score.data_ptr(), lengths.data_ptr(), strides, B, H, N, D, budget, first, last,
            ko.data_ptr(), vo.data_ptr(), so.data_ptr(), positions.data_ptr(), left.data_ptr())
+    if out is not None:
+        increment_version((ko, vo, so))
     return result

@@ -106,3 +106,50 @@ def test_combination_takes_no_memory_for_other_gradients(cuda_device):
     out = L.expert_combine(leaf.expand(T * k, H) * 1.0, w0, plan)
     assert torch.cuda.memory_allocated() - before < rows / 2
     assert out.grad_fn is not None
+
+
+def test_tensors_that_a_graph_kept_are_seen_to_change(cuda_device):
+    """Written in place, as by torch's own in-place operations: a backward pass that needs the
+    values from before raises instead of taking the new ones."""
+    gen = torch.Generator().manual_seed(4)
+    q, k, v = (torch.randn(s, generator=gen).to(torch.bfloat16).cuda()
+               for s in ((1, 1, 4, 16), (1, 2, 50, 16), (1, 2, 50, 16)))
+    n = torch.tensor([50], dtype=torch.int32).cuda()
+
+    def attend(**o):
+        return lambda x: L.attend_accumulate(q, k, v, n, **{name: x for name in o["into"]},
+                                             **({} if "score" in o["into"] else {"score": torch.zeros((1, 2, 50), device="cuda")}))
+
+    def evict(at):
+        def call(x):
+            out = [torch.zeros((1, 2, 8, 16), dtype=torch.bfloat16, device="cuda"),
+                   torch.zeros((1, 2, 8, 16), dtype=torch.bfloat16, device="cuda"),
+                   torch.zeros((1, 2, 8), device="cuda")]
+            out[at] = x
+            L.evict(k, v, torch.rand((1, 2, 50), device="cuda"), n, 8, out=tuple(out))
+        return call
+
+    rows = torch.zeros((1, 2, 8, 16), dtype=torch.bfloat16, device="cuda")
+    for write, x in ((attend(into=("score",)), torch.zeros((1, 2, 50), device="cuda")),
+                     (attend(into=("score_out",)), torch.zeros((1, 2, 50), device="cuda")),
+                     (attend(into=("out",)), torch.zeros((1, 1, 4, 16), dtype=torch.bfloat16, device="cuda")),
+                     (evict(0), rows.clone()), (evict(1), rows.clone()),
+                     (evict(2), torch.zeros((1, 2, 8), device="cuda"))):
+        w = torch.ones_like(x, requires_grad=True)
+        z = (w * x).sum()
+        before = x._version
+        write(x)
+        assert x._version > before
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            z.backward()
+        z = (w * x).sum()
+        z.backward()
+        assert torch.equal(w.grad, x)
+    # what is only read keeps its version; inference tensors have none
+    score, into = torch.zeros((1, 2, 50), device="cuda"), torch.zeros((1, 2, 50), device="cuda")
+    was = [t._version for t in (q, k, v, n, score)]
+    L.attend_accumulate(q, k, v, n, score, score_out=into)
+    L.evict(k, v, score, n, 8)
+    assert was == [t._version for t in (q, k, v, n, score)]
+    with torch.inference_mode():
+        L.attend_accumulate(q, k, v, n, torch.zeros((1, 2, 50), device="cuda"))
