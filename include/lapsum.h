@@ -530,13 +530,17 @@ int lapsum_expert_combine_backward_part(const void* dout, int dtype, int64_t ld,
  * for j < lengths[b]; scores behind are neither read nor written.  score_in NULL
  * reads as 0; it may be score_out itself (else they must not overlap).  A query
  * that sees no key gets out = 0 and adds nothing.  Cache rows behind lengths[b] may
- * hold anything.  `strides` (host, 13 entries, in elements): batch, head and token
- * stride of q; batch, head and row stride of k, then of v; batch and head stride
- * of score_in, then of score_out (the elements of a row, and a head's scores, are
- * consecutive; the stride of a dimension of one element is not read).  D is a multiple of 16 up to 256; q, k, v and out are 16-byte
- * aligned and their strides multiples of 8; Hq a multiple of Hkv.  Softmax
- * statistics, sums and scores are fp32.  ws: lapsum_attend_workspace_bytes(...)
- * bytes, 256-byte aligned (0: bad sizes).
+ * hold anything.  An infinity or NaN in a value row of the Sq tokens' own keys may make
+ * that element of the output NaN for the tokens before it too (0 times it is NaN), and an
+ * infinite value that has weight gives NaN.  `strides` (host, 13 entries, in elements):
+ * batch, head and token stride of q; batch, head and row stride of k, then of v; batch
+ * and head stride of score_in, then of score_out (the elements of a row, and a head's
+ * scores, are consecutive; the stride of a dimension of one element is not read).  D is
+ * a multiple of 16 up to 256; q, k, v and out are 16-byte aligned and their strides
+ * multiples of 8; Hq a multiple of Hkv.  Softmax statistics, sums and scores are fp32;
+ * weights reach the output to 2^-15 of themselves (bf16), or to 2^-22 of themselves and
+ * 2^-48 of the row's largest (fp16; 2^-36 of it for D > 128 past 16 rows a key).  ws:
+ * lapsum_attend_workspace_bytes(...) bytes, 256-byte aligned (0: bad sizes).
  */
 size_t lapsum_attend_workspace_bytes(int64_t B, int64_t Sq, int64_t Hq, int64_t Hkv, int64_t N,
                                      int64_t D);

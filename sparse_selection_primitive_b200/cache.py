@@ -53,7 +53,8 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
     that each key received from the Sq * Hq / Hkv queries of its head, or
     ``score_out`` gets the sum and ``score`` stays.
 
-    A token i sees the keys before lengths - Sq + i + 1; one that sees none gets 0.
+    A token i sees the keys before lengths - Sq + i + 1; one that sees none gets 0.  Values of
+    seen keys are to be finite: a NaN among the Sq tokens' own may reach the tokens before it.
     ``scale`` is D ** -0.5 by default.  D is a multiple of 16 up to 256; the tensors may
     be strided views whose rows start on 16 bytes.  No gradient."""
     ks, vs, ss = _check_caches(k, v, score, lengths, _HALF)

@@ -106,9 +106,9 @@ def route_experts(logits: torch.Tensor, k: int, *, score: str = "softmax", bias=
                   renormalize: bool = True, scale: float = 1.0):
     """(weights, experts), both (T, k), of the k experts with the largest keys per row.
 
-    ``logits`` (T, E) float32, bfloat16 or float16, E <= 1024.  The scores are a
-    ``softmax`` over the row or each logit's ``sigmoid``; ``bias`` (E, float32) is
-    added for the choice only and gets no gradient.  With ``top_groups`` < ``groups``
+    ``logits`` (T, E) float32, bfloat16 or float16, E <= 1024; k and ``groups`` are at most
+    32.  The scores are a ``softmax`` over the row or each logit's ``sigmoid``; ``bias`` (E,
+    float32) is added for the choice only and gets no gradient.  With ``top_groups`` < ``groups``
     the choice is limited to the groups whose ``group_top`` (1 or 2) largest keys have
     the largest sum.  The weights (float32, differentiable in the logits) are the chosen
     scores, by default divided by their sum, times ``scale``.  Equal keys go to the
