@@ -17,7 +17,7 @@
 // More than kKeepRows rows a key fill the M side themselves (attend_wide_kernel).
 //
 // 32 x 8192 keys x 8 heads of 128, 8 rows a key: 179 us at full length (169 us of bytes), DRAM
-// bound.  2 x 32768 x 8, 128 rows: 70 us for the outputs (42 us of bytes, 21 of products), 34 for
+// bound.  2 x 32768 x 8, 128 rows: 72 us for the outputs (42 us of bytes, 21 of products), 35 for
 // the scores.  Matrix instructions issued from a branch on the lane number, not by an elected
 // thread, cost 15 us of the one and 8 of the other.
 #include <atomic>

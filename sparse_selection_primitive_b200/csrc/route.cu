@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 //     sum_j w_j (u_i - u_j) = W (u_i - u_0) - sum_j w_j (u_j - u_0),
 // one sum for all i: for i = 0 the dominating term is exactly 0, and as w_0 >= W / k, the two
 // parts are at most 2 k + 1 times the sum of magnitudes for any i.
-// A row whose weights are NaN gets NaN.  9.5 us for 16384 x 256 fp32 (2.8 us of bytes); carrying
+// A row whose weights are NaN gets NaN.  9.0 us for 16384 x 256 fp32 (2.8 us of bytes); carrying
 // the chosen terms to the lanes that own their experts instead of storing them on top took 19.
 template <class T, int V>
 __global__ void __launch_bounds__(kRouteWarps * 32)
