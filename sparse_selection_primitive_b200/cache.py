@@ -73,6 +73,9 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
         score_out, outs = score, ss
     else:
         need(score_out, "score_out", _F32, 3, k.device)
+        if score_out.requires_grad:
+            no_gradient("attend_accumulate")
+        no_tangents("attend_accumulate", score_out)
         outs = score_out.stride()
         if score_out.shape != score.shape or N > 1 and outs[2] != 1:
             raise ValueError("score_out must have score's shape, consecutive in its last dimension")
@@ -87,6 +90,9 @@ def attend_accumulate(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lengths
     else:
         written = score_out, out
         need(out, "out", (q.dtype,), 4, q.device)
+        if out.requires_grad:
+            no_gradient("attend_accumulate")
+        no_tangents("attend_accumulate", out)
         if out.shape != q.shape or not out.is_contiguous():
             raise ValueError("out must be contiguous and have q's shape")
         if any(overlap(out, x) for x in (q, k, v, score, score_out)):
@@ -147,6 +153,9 @@ def evict(k: torch.Tensor, v: torch.Tensor, score: torch.Tensor, lengths: torch.
         need(ko, "out[0]", (k.dtype,), 4, k.device)
         need(vo, "out[1]", (k.dtype,), 4, k.device)
         need(so, "out[2]", (torch.float32,), 3, k.device)
+        if ko.requires_grad or vo.requires_grad or so.requires_grad:
+            no_gradient("evict")
+        no_tangents("evict", ko, vo, so)
         for x, d in ((ko, (D,)), (vo, (D,)), (so, ())):
             if x.shape[:2] != (B, H) or x.shape[2] < budget or tuple(x.shape[3:]) != d or \
                     x.shape[-1] > 1 and x.stride(-1) != 1 or not distinct(x):

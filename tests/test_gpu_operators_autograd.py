@@ -153,3 +153,26 @@ def test_tensors_that_a_graph_kept_are_seen_to_change(cuda_device):
     assert was == [t._version for t in (q, k, v, n, score)]
     with torch.inference_mode():
         L.attend_accumulate(q, k, v, n, torch.zeros((1, 2, 50), device="cuda"))
+
+
+def test_results_into_tensors_that_require_a_gradient_are_refused(cuda_device):
+    """As torch's own out= arguments; without grad mode, or detached, they are filled."""
+    q, k, v = (torch.randn(s).to(torch.bfloat16).cuda() for s in ((1, 1, 4, 16), (1, 2, 50, 16), (1, 2, 50, 16)))
+    n, score = torch.tensor([50], dtype=torch.int32).cuda(), torch.rand((1, 2, 50), device="cuda")
+    rooms = [torch.zeros((1, 2, 8, 16), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    rooms.append(torch.zeros((1, 2, 8), device="cuda"))
+
+    def evict(at):
+        return lambda x: L.evict(k, v, score, n, 8, out=tuple(x if i == at else r for i, r in enumerate(rooms)))
+
+    for call, x in ((lambda x: L.attend_accumulate(q, k, v, n, score, score_out=x), torch.zeros_like(score)),
+                    (lambda x: L.attend_accumulate(q, k, v, n, score, out=x), torch.zeros_like(q)),
+                    (evict(0), rooms[0].clone()), (evict(1), rooms[1].clone()), (evict(2), rooms[2].clone())):
+        leaf = x.requires_grad_(True)
+        with pytest.raises(RuntimeError, match="no gradient"):
+            call(leaf)
+        with torch.no_grad():
+            call(leaf)
+        call(leaf.detach())
+        with fw.dual_level(), torch.no_grad(), pytest.raises(NotImplementedError):
+            call(fw.make_dual(leaf.detach(), torch.ones_like(leaf)))
